@@ -282,6 +282,195 @@ int sdq_validate_swiglu_q8_1(const void* gate, int64_t ld_gate, const void* up, 
                              int64_t rows, int64_t inter);
 
 /*
+ * ---- Around the projections: RMS norm, 4-bit quantizer, 4-bit product --------
+ *
+ * Formats of these entries (OR-ed; SDQ_FMT_E4M3 and SDQ_FMT_E8M0 as above):
+ *   SDQ_FMT_E2M1        4-bit codes: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit
+ *                       (OCP Microscaling E2M1), two to a byte, the lower index
+ *                       in the low four bits
+ *   SDQ_FMT_SCALE_E4M3  E4M3 scales, one for 16 values, times a scale per tensor
+ *                       (with SDQ_FMT_E8M0 instead: one for 32 values)
+ *   SDQ_FMT_WEIGHT_F32  the norm's weight is fp32 (else bf16)
+ *   SDQ_FMT_OUT_F32     the product's output is fp32 (else bf16)
+ *
+ * A group of values becomes a scale and codes so:
+ *   8-bit codes          as sdq_fuse_format: scale = fl32(amax / Qmax), or the
+ *                        smallest power of two not below it (E8M0); code =
+ *                        round-to-nearest-even of value * (1 / scale)
+ *   E2M1, E8M0 scales    the smallest power of two not below fl32(amax / 6)
+ *   E2M1, E4M3 scales    scale = E4M3(fl32(amax / fl32(6 g))), at least 2^-9 and
+ *                        at most 448, g the scale per tensor (finite and
+ *                        positive; a NULL pointer: 1); a code of 1 stands for
+ *                        fl32(scale * g); code = round-to-nearest-even of the
+ *                        quotient, saturated to +-6.  A g of amax(tensor) / 2688
+ *                        uses the whole range of the scales.
+ *   an all-zero group    scale 1, codes 0 (E4M3 and E2M1 zeros keep their sign)
+ *   a group holding a NaN or an infinity: scale NaN (fp32 NaN, E8M0 0xFF, E4M3
+ *                        0x7F), codes 0: all of the group reads back as NaN
+ *
+ * Scale tiles: the scales of 4-bit operands lie as the tensor cores read them,
+ * in tiles of 128 rows x 4 groups, 512 bytes each, the tiles of 128 rows side by
+ * side along k: the scale of row r and group j is byte
+ *   ((r / 128) * ceil(groups / 4) + j / 4) * 512
+ *     + (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4.
+ * sdq_fp4_scale_bytes gives the size.  Bytes of rows past the last are neither
+ * written nor used; bytes of groups past the last (when 4 does not divide their
+ * number) are written as 0 and have to be 0 in tiles made elsewhere.
+ *
+ * k (channels of 4-bit rows) is a multiple of SDQ_FP4_K_MULTIPLE.
+ */
+#define SDQ_FMT_E2M1 8u
+#define SDQ_FMT_SCALE_E4M3 16u
+#define SDQ_FMT_WEIGHT_F32 32u
+#define SDQ_FMT_OUT_F32 64u
+#define SDQ_FP4_K_MULTIPLE 32
+
+/*
+ * sdq_rmsnorm_quant -- RMS norm with the residual's addition, its rows
+ * quantized:
+ *   h[m, k] = bf16(x[m, k] + residual[m, k])   (h = x without a residual)
+ *   rstd[m] = 1 / sqrt(mean_k h[m, k]^2 + eps)
+ *   y[m, k] = h[m, k] * rstd[m] * weight[k]    fp32; codes and scales are y's
+ *   x         device, bf16 [rows, channels], 16-byte aligned, ld a multiple of 8
+ *   residual  likewise, or NULL
+ *   weight    bf16 or (SDQ_FMT_WEIGHT_F32) fp32 [channels], 16-byte aligned
+ *   h         bf16 [rows, channels], written with a residual, else ignored; may
+ *             be x or residual itself (same pointer and ld)
+ *   q         codes: bytes [rows, channels], or with SDQ_FMT_E2M1 [rows,
+ *             channels / 2]; 16-byte aligned, ld (bytes) a multiple of 16
+ *   s         scales [rows, ceil(channels / group_size)] (fp32, 4-byte aligned,
+ *             or E8M0 bytes), ld_s apart; with SDQ_FMT_E2M1 scale tiles (16-byte
+ *             aligned, ld_s ignored)
+ *   y         optional (NULL): y rounded to bf16 [rows, channels]
+ *   rstd      optional (NULL): fp32 [rows], what the backward needs
+ *   global_scale  one fp32 on the device (SDQ_FMT_SCALE_E4M3), or NULL for 1
+ *   group_size  8-bit codes: 32, 64, 128 or 256 channels a scale, or 0 for one
+ *             scale a row; E2M1: 32 with E8M0 scales, 16 with E4M3 scales
+ *   format    SDQ_FMT_E4M3, or SDQ_FMT_E2M1, or neither (INT8); SDQ_FMT_E8M0 or
+ *             not (fp32 scales), for E2M1 exactly one of SDQ_FMT_E8M0 and
+ *             SDQ_FMT_SCALE_E4M3; SDQ_FMT_WEIGHT_F32
+ *   rows 0 <= rows <= SDQ_MAX_M (0: no-op); channels a multiple of
+ *   SDQ_K_MULTIPLE (E2M1: SDQ_FP4_K_MULTIPLE), at most SDQ_MAX_K.
+ * One kernel on `stream`; allocates nothing.  Errors as sdq_fuse_strided.
+ */
+int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                      const void* weight, void* h, int64_t ld_h, void* q, int64_t ld_q, void* s,
+                      int64_t ld_s, void* y, int64_t ld_y, float* rstd, const float* global_scale,
+                      int64_t rows, int64_t channels, int32_t group_size, uint32_t format, float eps,
+                      void* stream);
+
+/* The argument checks of sdq_rmsnorm_quant alone: no CUDA call, no launch. */
+int sdq_validate_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                               const void* weight, const void* h, int64_t ld_h, const void* q,
+                               int64_t ld_q, const void* s, int64_t ld_s, const void* y, int64_t ld_y,
+                               const float* rstd, const float* global_scale, int64_t rows,
+                               int64_t channels, int32_t group_size, uint32_t format);
+
+/*
+ * sdq_rmsnorm_backward -- the gradients of that norm, codes taken as the
+ * identity (straight through):
+ *   n = h * rstd,  g = grad_y * weight
+ *   grad_x[m, k]   = bf16(rstd[m] * (g - n * mean_k(g * n)) + grad_h[m, k])
+ *   grad_weight[k] = sum_m grad_y[m, k] * n[m, k]                       fp32
+ * grad_x is the gradient of x and of residual alike.
+ *   grad_y, h      bf16 [rows, channels]; h as sdq_rmsnorm_quant wrote it (x
+ *                  without a residual); rstd fp32 [rows] likewise
+ *   grad_h         bf16, the gradient that reaches h past the norm, or NULL
+ *   grad_x         bf16 (written); may be grad_y, h or grad_h itself
+ *   grad_weight    fp32 [channels] (written; zeros when rows is 0)
+ *   format         SDQ_FMT_WEIGHT_F32 or 0
+ *   workspace      device memory of sdq_rmsnorm_backward_workspace_bytes(rows,
+ *                  channels) bytes, 16-byte aligned; calls that overlap (on other
+ *                  streams, or two graphs replayed at once) need one each
+ * Two kernels on `stream`, without atomics: equal inputs give equal bits.
+ */
+int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, int64_t ld_h,
+                         const void* weight, const float* rstd, const void* grad_h, int64_t ld_grad_h,
+                         void* grad_x, int64_t ld_grad_x, float* grad_weight, int64_t rows,
+                         int64_t channels, uint32_t format, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* The argument checks of sdq_rmsnorm_backward alone: no CUDA call, no launch. */
+int sdq_validate_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, int64_t ld_h,
+                                  const void* weight, const float* rstd, const void* grad_h,
+                                  int64_t ld_grad_h, const void* grad_x, int64_t ld_grad_x,
+                                  const float* grad_weight, int64_t rows, int64_t channels,
+                                  uint32_t format, const void* workspace, size_t workspace_bytes);
+
+/* Workspace of sdq_rmsnorm_backward; 0 for sizes it does not take. */
+size_t sdq_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t channels);
+
+/*
+ * sdq_quantize_fp4 -- bf16 [rows, channels] to 4-bit codes and scale tiles:
+ * along the rows (q, s), along the columns of x, transposed (q_t, s_t), or both
+ * in one pass (the forms the products of a forward, a data gradient and a weight
+ * gradient take).
+ *   x      device, bf16, 16-byte aligned, ld a multiple of 8 elements
+ *   q      codes [rows, channels / 2] bytes, 16-byte aligned, ld (bytes) a
+ *          multiple of 16; s its scale tiles.  NULL: not written.
+ *   q_t    codes [channels, up32(rows) / 2], up32 rounding up to a multiple of
+ *          32: the rows that are missing count as zeros; s_t its scale tiles.
+ *          NULL: not written.
+ *   global_scale  one fp32 on the device (SDQ_FMT_SCALE_E4M3), or NULL for 1
+ *   format SDQ_FMT_E8M0 or SDQ_FMT_SCALE_E4M3
+ * One kernel on `stream`; allocates nothing.
+ */
+int sdq_quantize_fp4(const void* x, int64_t ld_x, void* q, int64_t ld_q, void* s, void* q_t,
+                     int64_t ld_q_t, void* s_t, const float* global_scale, int64_t rows,
+                     int64_t channels, uint32_t format, void* stream);
+
+/* The argument checks of sdq_quantize_fp4 alone: no CUDA call, no launch. */
+int sdq_validate_quantize_fp4(const void* x, int64_t ld_x, const void* q, int64_t ld_q, const void* s,
+                              const void* q_t, int64_t ld_q_t, const void* s_t,
+                              const float* global_scale, int64_t rows, int64_t channels,
+                              uint32_t format);
+
+/*
+ * sdq_dequantize_fp4 -- codes and scale tiles back to bf16:
+ *   out[r, k] = bf16(fl32(code * unit)), unit = scale (E8M0) or fl32(scale * g).
+ * A NaN scale gives NaN.  Arguments as sdq_quantize_fp4; out bf16 [rows,
+ * channels], 16-byte aligned, ld a multiple of 8.
+ */
+int sdq_dequantize_fp4(const void* q, int64_t ld_q, const void* s, const float* global_scale, void* out,
+                       int64_t ld_out, int64_t rows, int64_t channels, uint32_t format, void* stream);
+
+/* The argument checks of sdq_dequantize_fp4 alone: no CUDA call, no launch. */
+int sdq_validate_dequantize_fp4(const void* q, int64_t ld_q, const void* s, const float* global_scale,
+                                const void* out, int64_t ld_out, int64_t rows, int64_t channels,
+                                uint32_t format);
+
+/* Bytes of the scale tiles of [rows, k] 4-bit codes (format SDQ_FMT_E8M0 or
+ * SDQ_FMT_SCALE_E4M3); 0 for sizes these entries do not take. */
+int64_t sdq_fp4_scale_bytes(int64_t rows, int64_t k, uint32_t format);
+
+/*
+ * sdq_matmul_fp4 -- the product of two 4-bit operands on the tensor cores:
+ *   out[i, j] = a_global * b_global * sum_k value_a[i, k] * value_b[j, k]
+ * summed in fp32, rounded once (bf16) or not at all (SDQ_FMT_OUT_F32).  With the
+ * transposed codes of sdq_quantize_fp4 it is also the data gradient (gradient
+ * times transposed weight) and the weight gradient (transposed gradient times
+ * transposed activations).
+ *   a      codes [m, k / 2], 16-byte aligned, ld (bytes) a multiple of 16; a_s
+ *          its scale tiles; a_global one fp32 on the device or NULL for 1
+ *   b      codes [n, k / 2], likewise
+ *   out    bf16 or fp32 [m, n], aligned to its element, any ld >= n
+ *   m, n   at least 0 (0: no-op), at most SDQ_MAX_M; k a multiple of
+ *          SDQ_FP4_K_MULTIPLE, at most SDQ_MAX_K
+ *   format SDQ_FMT_E8M0 or SDQ_FMT_SCALE_E4M3, of both operands; SDQ_FMT_OUT_F32
+ * One kernel on `stream`; allocates nothing.  Its waits are bounded: see
+ * sdq_device_status.
+ */
+int sdq_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_global, const void* b,
+                   int64_t ld_b, const void* b_s, const float* b_global, void* out, int64_t ld_out,
+                   int64_t m, int64_t n, int64_t k, uint32_t format, void* stream);
+
+/* The argument checks of sdq_matmul_fp4 alone: no CUDA call, no launch. */
+int sdq_validate_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_global,
+                            const void* b, int64_t ld_b, const void* b_s, const float* b_global,
+                            const void* out, int64_t ld_out, int64_t m, int64_t n, int64_t k,
+                            uint32_t format);
+
+/*
  * sdq_fuse_host -- the op on HOST buffers (same shapes and layouts as
  * sdq_fuse; page-locked host memory gives overlapped copies, pageable memory
  * works but copies synchronously).  The rows are processed in chunks through

@@ -14,6 +14,11 @@ Other output formats (include/sdq.h, SDQ_FMT_*) follow from the output
 tensors' dtypes: float8_e4m3fn codes (OCP FP8 E4M3), uint8 or float8_e8m0fnu
 scales (E8M0 powers of two); ``y_scale_layout="mg_k"`` gives y_s_t as
 [ceil(M/128), K].
+
+Around the projections next to it: ``rmsnorm_quant`` / ``rmsnorm_backward`` (RMS
+norm with the residual's addition, rows in 8- or 4-bit codes), ``quantize_fp4`` /
+``dequantize_fp4`` and ``matmul_fp4`` (microscaled 4-bit operands and their
+product).
 """
 from __future__ import annotations
 
@@ -27,6 +32,14 @@ from ._lib import (FMT_E4M3, FMT_E8M0, FMT_YS_MG_K, LIB_PATH, SdqError, Status, 
                    sdq_fuse_strided, sdq_validate_int8_grad_y,
                    sdq_swiglu_q8_1, sdq_validate, sdq_validate_format, sdq_validate_strided,
                    sdq_validate_swiglu_q8_1, status_string, version)
+from ._check import _rows
+from .lowbit import (dequantize_fp4, fp4_scale_shape, matmul_fp4, quantize_fp4, rmsnorm_backward,
+                     rmsnorm_quant)
+from ._lib import (FMT_E2M1, FMT_OUT_F32, FMT_SCALE_E4M3, FMT_WEIGHT_F32, sdq_dequantize_fp4,
+                   sdq_fp4_scale_bytes, sdq_matmul_fp4, sdq_quantize_fp4, sdq_rmsnorm_backward,
+                   sdq_rmsnorm_backward_workspace_bytes, sdq_rmsnorm_quant, sdq_validate_dequantize_fp4,
+                   sdq_validate_matmul_fp4, sdq_validate_quantize_fp4, sdq_validate_rmsnorm_backward,
+                   sdq_validate_rmsnorm_quant)
 
 __all__ = [
     "silu_dot_fwd_bwd_quant_fuse", "silu_dot_fwd_bwd_quant_fuse_split",
@@ -38,6 +51,11 @@ __all__ = [
     "sdq_fuse_host_workspace_bytes", "sdq_validate",
     "sdq_device_status", "SdqError", "Status", "status_string", "last_cuda_error", "version",
     "LIB_PATH", "GROUP_SIZE", "GROUP_SIZES", "K_MULTIPLE",
+    "rmsnorm_quant", "rmsnorm_backward", "quantize_fp4", "dequantize_fp4", "matmul_fp4", "fp4_scale_shape",
+    "sdq_rmsnorm_quant", "sdq_validate_rmsnorm_quant", "sdq_rmsnorm_backward", "sdq_validate_rmsnorm_backward",
+    "sdq_rmsnorm_backward_workspace_bytes", "sdq_quantize_fp4", "sdq_validate_quantize_fp4",
+    "sdq_dequantize_fp4", "sdq_validate_dequantize_fp4", "sdq_matmul_fp4", "sdq_validate_matmul_fp4",
+    "sdq_fp4_scale_bytes", "FMT_E2M1", "FMT_SCALE_E4M3", "FMT_WEIGHT_F32", "FMT_OUT_F32",
 ]
 
 GROUP_SIZE = 128
@@ -89,25 +107,6 @@ def _infer(kind: str, given: Optional[str], t: torch.Tensor, table) -> str:
     if given not in table:
         raise ValueError(f"unknown {kind} format {given!r}")
     return given
-
-
-def _rows(name: str, t: torch.Tensor, shape, dtypes, want_cuda: bool, device) -> int:
-    """Check a 2-D row-major operand (rows may be padded: stride(0) >= its
-    row); returns its leading dimension in elements."""
-    if t.dim() != 2 or tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit stride along its rows")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} < row length {t.shape[1]})")
-    if not want_cuda and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous for the host-buffer entry points")
-    if want_cuda and (not t.is_cuda or t.device != device):
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if not want_cuda and t.is_cuda:
-        raise ValueError(f"{name} must be a host tensor")
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1])
 
 
 def _check_group(K: int, group_size: int, want_cuda: bool):

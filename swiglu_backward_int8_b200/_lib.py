@@ -46,6 +46,24 @@ _lib.sdq_swiglu_q8_1.argtypes = [_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I6
 _lib.sdq_swiglu_q8_1.restype = ctypes.c_int
 _lib.sdq_validate_swiglu_q8_1.argtypes = [_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64]
 _lib.sdq_validate_swiglu_q8_1.restype = ctypes.c_int
+_F32 = ctypes.c_float
+_U32 = ctypes.c_uint32
+_NORM = [_P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I32, _U32]
+_NORM_BWD = [_P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _U32, _P, ctypes.c_size_t]
+_QUANT = [_P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _U32]
+_DEQUANT = [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _U32]
+_MATMUL = [_P, _I64, _P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _U32]
+for _name, _args, _more in (("rmsnorm_quant", _NORM, [_F32, _P]), ("rmsnorm_backward", _NORM_BWD, [_P]),
+                            ("quantize_fp4", _QUANT, [_P]), ("dequantize_fp4", _DEQUANT, [_P]),
+                            ("matmul_fp4", _MATMUL, [_P])):
+    getattr(_lib, f"sdq_{_name}").argtypes = _args + _more
+    getattr(_lib, f"sdq_{_name}").restype = ctypes.c_int
+    getattr(_lib, f"sdq_validate_{_name}").argtypes = _args
+    getattr(_lib, f"sdq_validate_{_name}").restype = ctypes.c_int
+_lib.sdq_rmsnorm_backward_workspace_bytes.argtypes = [_I64, _I64]
+_lib.sdq_rmsnorm_backward_workspace_bytes.restype = ctypes.c_size_t
+_lib.sdq_fp4_scale_bytes.argtypes = [_I64, _I64, _U32]
+_lib.sdq_fp4_scale_bytes.restype = _I64
 _lib.sdq_fuse_host.argtypes = [_P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _P, ctypes.c_size_t, _I64, _P]
 _lib.sdq_fuse_host.restype = ctypes.c_int
 _lib.sdq_fuse_host_workspace_bytes.argtypes = [_I64, _I64, _I64]
@@ -83,6 +101,11 @@ class Status(enum.IntEnum):
 FMT_E4M3 = 1       # codes are OCP FP8 E4M3 bytes
 FMT_E8M0 = 2       # scales are E8M0 bytes (powers of two)
 FMT_YS_MG_K = 4    # y_s_t is [ceil(M/128), K]
+# Formats of the norm, the 4-bit quantizer and the product (with FMT_E4M3, FMT_E8M0).
+FMT_E2M1 = 8         # codes are 4-bit E2M1, two to a byte
+FMT_SCALE_E4M3 = 16  # scales are E4M3 bytes for 16 values, times a scale per tensor
+FMT_WEIGHT_F32 = 32  # the norm's weight is fp32
+FMT_OUT_F32 = 64     # the product's output is fp32
 
 
 class SdqError(RuntimeError):
@@ -246,3 +269,38 @@ def sdq_fuse_host_workspace_bytes(M: int, K: int, chunk_rows: int = 0) -> int:
 def sdq_device_status(stream: Optional[int] = None) -> int:
     """Synchronize `stream`, read and clear the device status word."""
     return int(_lib.sdq_device_status(stream or 0))
+
+
+def _entry(name: str, doc: str):
+    """The raw-pointer form of an entry point, raising SdqError on a status,
+    and that of its argument checks, returning the status.  The arguments are
+    the C function's, in its order (addresses as ints, None for NULL)."""
+    call, check = getattr(_lib, name), getattr(_lib, name.replace("sdq_", "sdq_validate_"))
+
+    def run(*args) -> None:
+        status = call(*args)
+        if status:
+            raise SdqError(status, name)
+
+    def validate(*args) -> int:
+        return int(check(*args))
+
+    run.__name__, run.__doc__ = name, f"Raw-pointer form of {doc} (include/sdq.h: {name})."
+    validate.__name__ = check.__name__
+    validate.__doc__ = f"Argument checks of {name} only (no CUDA call); returns the status code."
+    return run, validate
+
+
+sdq_rmsnorm_quant, sdq_validate_rmsnorm_quant = _entry("sdq_rmsnorm_quant", "the quantizing RMS norm")
+sdq_rmsnorm_backward, sdq_validate_rmsnorm_backward = _entry("sdq_rmsnorm_backward", "the norm's gradients")
+sdq_quantize_fp4, sdq_validate_quantize_fp4 = _entry("sdq_quantize_fp4", "the 4-bit quantizer")
+sdq_dequantize_fp4, sdq_validate_dequantize_fp4 = _entry("sdq_dequantize_fp4", "reading 4-bit codes back")
+sdq_matmul_fp4, sdq_validate_matmul_fp4 = _entry("sdq_matmul_fp4", "the product of two 4-bit operands")
+
+
+def sdq_rmsnorm_backward_workspace_bytes(rows: int, channels: int) -> int:
+    return int(_lib.sdq_rmsnorm_backward_workspace_bytes(rows, channels))
+
+
+def sdq_fp4_scale_bytes(rows: int, k: int, format: int) -> int:
+    return int(_lib.sdq_fp4_scale_bytes(rows, k, format))

@@ -4,15 +4,19 @@
 
 (run it as a script: importing the package needs the library it builds)
 
-nvcc compiles ``csrc/sdq_api.cu`` (host API + the fused kernel) and
-``csrc/fwd_api.cu`` (the forward-side SwiGLU + q8_1 kernel) into a shared
-library with a C ABI (``include/sdq.h``); the CUDA runtime is linked
+nvcc compiles ``csrc/sdq_api.cu`` (host API + the fused kernel),
+``csrc/fwd_api.cu`` (the forward-side SwiGLU + q8_1 kernel),
+``csrc/norm_api.cu`` (the quantizing RMS norm) and ``csrc/fp4_api.cu`` (the
+4-bit quantizer and product), each in a process of its own, and links them into
+a shared library with a C ABI (``include/sdq.h``); the CUDA runtime is linked
 statically and the driver's tensor-map encoder is looked up at run time, so
 the library needs only the NVIDIA driver at load time.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -22,13 +26,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsdq.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("sdq_api.cu", "fwd_api.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("sdq_kernel.cuh", "sdq_ptx.cuh", "fwd_kernel.cuh")] + [
-    os.path.join(INCLUDE, "sdq.h")]
+OBJECTS = os.path.join(PKG, "_build")   # one object a source, kept for the next build
+SOURCES = [os.path.join(CSRC, f) for f in ("sdq_api.cu", "fwd_api.cu", "norm_api.cu", "fp4_api.cu")]
+DEPS = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)) + [os.path.join(INCLUDE, "sdq.h")]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2",
-              "-shared", "-I", INCLUDE, "-I", CSRC]
+              "-I", INCLUDE, "-I", CSRC]
 
 
 def nvcc() -> str:
@@ -38,18 +42,50 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libsdq.so if it is missing or older than its sources."""
-    if (not force and os.path.exists(LIB)
-            and os.path.getmtime(LIB) >= max(os.path.getmtime(f) for f in DEPS)):
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else []), *SOURCES, "-o", tmp]
+def _run(cmd, verbose: bool) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     if verbose:
         sys.stderr.write(r.stdout + r.stderr)
+
+
+def _includes(path: str) -> set:
+    """The source and the files of this repository that it includes."""
+    found, todo = set(), [path]
+    while todo:
+        f = todo.pop()
+        if f in found:
+            continue
+        found.add(f)
+        with open(f) as src:
+            for name in re.findall(r'^#include "([^"]+)"', src.read(), flags=re.M):
+                todo += [p for d in (CSRC, INCLUDE) if os.path.exists(p := os.path.join(d, name))]
+    return found
+
+
+def _compile(source: str, obj: str, force: bool, verbose: bool) -> None:
+    """Compile one source unless its object is newer than all that goes into it."""
+    used = _includes(source) | {os.path.abspath(__file__)}
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(f) for f in used):
+        return
+    tmp = f"{obj}.tmp{os.getpid()}"
+    _run([nvcc(), *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else []), "-c", source, "-o", tmp], verbose)
+    os.replace(tmp, obj)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile libsdq.so if it is missing or older than its sources."""
+    if (not force and os.path.exists(LIB)
+            and os.path.getmtime(LIB) >= max(os.path.getmtime(f) for f in DEPS)):
+        return LIB
+    os.makedirs(OBJECTS, exist_ok=True)
+    objects = [os.path.join(OBJECTS, os.path.basename(s) + ".o") for s in SOURCES]
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+        for _ in pool.map(lambda so: _compile(*so, force, verbose), zip(SOURCES, objects)):
+            pass
+    tmp = LIB + f".tmp{os.getpid()}"
+    _run([nvcc(), *ARCH, "-shared", *objects, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
 

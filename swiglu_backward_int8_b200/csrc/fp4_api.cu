@@ -1,0 +1,211 @@
+// C ABI of the microscaled 4-bit quantizer and product (declared in
+// include/sdq.h): argument validation and the launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "fp4_kernel.cuh"
+#include "fp4_matmul.cuh"
+#include "sdq.h"
+#include "sdq_internal.h"
+
+namespace {
+
+using sdq::quant::Scales;
+
+bool misaligned(const void* p, uintptr_t mask) { return reinterpret_cast<uintptr_t>(p) & mask; }
+
+// Exactly one scale format.
+bool format_ok(uint32_t f, uint32_t more = 0) {
+  if (f & ~(SDQ_FMT_E8M0 | SDQ_FMT_SCALE_E4M3 | more)) return false;
+  return ((f & SDQ_FMT_E8M0) != 0) != ((f & SDQ_FMT_SCALE_E4M3) != 0);
+}
+
+bool length_ok(int64_t k) { return k >= 1 && k <= SDQ_MAX_K && k % SDQ_FP4_K_MULTIPLE == 0; }
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int group_of(uint32_t f) { return f & SDQ_FMT_E8M0 ? 32 : 16; }
+int64_t tiles_of(int64_t k, uint32_t f) { return (k / group_of(f) + 3) / 4; }   // scale tiles along k
+
+int launch(const void* kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+  return e == cudaSuccess ? SDQ_OK : sdq_internal::cuda_fail(e);
+}
+
+template <Scales S>
+const void* quantize_kernel(bool rows, bool cols) {
+  if (rows && cols) return reinterpret_cast<const void*>(sdq::fp4::quantize_kernel<S, true, true>);
+  return rows ? reinterpret_cast<const void*>(sdq::fp4::quantize_kernel<S, true, false>)
+              : reinterpret_cast<const void*>(sdq::fp4::quantize_kernel<S, false, true>);
+}
+
+struct MatmulKernel {
+  const void* fn;
+  size_t smem;
+  int n;
+};
+
+template <Scales S, int kN>
+MatmulKernel matmul_of() {
+  return {reinterpret_cast<const void*>(sdq::mm4::matmul_kernel<S, kN>), sdq::mm4::Shape<S, kN>::kSmem, kN};
+}
+
+template <Scales S>
+MatmulKernel matmul_for(int64_t n) {
+  return n <= 16 ? matmul_of<S, 16>() : n <= 32 ? matmul_of<S, 32>() : n <= 64 ? matmul_of<S, 64>()
+       : n <= 128 ? matmul_of<S, 128>() : matmul_of<S, 256>();
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sdq_fp4_scale_bytes(int64_t rows, int64_t k, uint32_t format) {
+  if (rows < 0 || rows > SDQ_MAX_M || !length_ok(k) || !format_ok(format)) return 0;
+  return (rows + 127) / 128 * tiles_of(k, format) * 512;
+}
+
+int sdq_validate_quantize_fp4(const void* x, int64_t ld_x, const void* q, int64_t ld_q, const void* s,
+                              const void* q_t, int64_t ld_q_t, const void* s_t, const float* global_scale,
+                              int64_t rows, int64_t channels, uint32_t format) {
+  if (!format_ok(format)) return SDQ_ERR_FORMAT;
+  if (rows < 0 || rows > SDQ_MAX_M || !length_ok(channels)) return SDQ_ERR_SHAPE;
+  if ((rows + 127) / 128 * ((channels + 127) / 128) > INT32_MAX) return SDQ_ERR_SHAPE;
+  if (rows == 0) return SDQ_OK;
+  if (!x || (!q && !q_t) || (q && !s) || (q_t && !s_t)) return SDQ_ERR_NULL;
+  if (ld_x < channels || ld_x > SDQ_MAX_LD) return SDQ_ERR_STRIDE;
+  if (q && (ld_q < channels / 2 || ld_q > SDQ_MAX_LD)) return SDQ_ERR_STRIDE;
+  if (q_t && (ld_q_t < up(rows, 32) / 2 || ld_q_t > SDQ_MAX_LD)) return SDQ_ERR_STRIDE;
+  if (misaligned(x, 15) || (ld_x & 7) || misaligned(global_scale, 3)) return SDQ_ERR_ALIGN;
+  if (q && (misaligned(q, 15) || (ld_q & 15) || misaligned(s, 15))) return SDQ_ERR_ALIGN;
+  if (q_t && (misaligned(q_t, 15) || (ld_q_t & 15) || misaligned(s_t, 15))) return SDQ_ERR_ALIGN;
+  return SDQ_OK;
+}
+
+int sdq_quantize_fp4(const void* x, int64_t ld_x, void* q, int64_t ld_q, void* s, void* q_t, int64_t ld_q_t, void* s_t,
+                     const float* global_scale, int64_t rows, int64_t channels, uint32_t format, void* stream) {
+  const int st = sdq_validate_quantize_fp4(x, ld_x, q, ld_q, s, q_t, ld_q_t, s_t, global_scale, rows, channels, format);
+  if (st != SDQ_OK || rows == 0) return st;
+  sdq::fp4::QuantParams p = {};
+  p.x = static_cast<const uint8_t*>(x);
+  p.q = static_cast<uint8_t*>(q);
+  p.s = static_cast<uint8_t*>(s);
+  p.qt = static_cast<uint8_t*>(q_t);
+  p.st = static_cast<uint8_t*>(s_t);
+  p.global = global_scale;
+  p.rows = rows;
+  p.ld_x = ld_x;
+  p.ld_q = ld_q;
+  p.ld_qt = ld_q_t;
+  p.rows_padded = up(rows, 32);
+  p.channels = static_cast<int32_t>(channels);
+  p.tiles_k = static_cast<int32_t>(tiles_of(channels, format));
+  p.tiles_m = tiles_of(p.rows_padded, format);
+  p.grid_k = static_cast<int32_t>((channels + 127) / 128);
+  const unsigned grid = static_cast<unsigned>((rows + 127) / 128 * p.grid_k);
+  void* args[] = {&p};
+  return launch(format & SDQ_FMT_E8M0 ? quantize_kernel<Scales::kE8M0>(q, q_t) : quantize_kernel<Scales::kE4M3>(q, q_t),
+                grid, sdq::fp4::kThreads, 0, static_cast<cudaStream_t>(stream), args);
+}
+
+int sdq_validate_dequantize_fp4(const void* q, int64_t ld_q, const void* s, const float* global_scale, const void* out,
+                                int64_t ld_out, int64_t rows, int64_t channels, uint32_t format) {
+  if (!format_ok(format)) return SDQ_ERR_FORMAT;
+  if (rows < 0 || rows > SDQ_MAX_M || !length_ok(channels)) return SDQ_ERR_SHAPE;
+  if (rows == 0) return SDQ_OK;
+  if (!q || !s || !out) return SDQ_ERR_NULL;
+  if (ld_q < channels / 2 || ld_q > SDQ_MAX_LD || ld_out < channels || ld_out > SDQ_MAX_LD) return SDQ_ERR_STRIDE;
+  if (misaligned(q, 15) || (ld_q & 15) || misaligned(s, 15) || misaligned(out, 15) || (ld_out & 7) ||
+      misaligned(global_scale, 3))
+    return SDQ_ERR_ALIGN;
+  return SDQ_OK;
+}
+
+int sdq_dequantize_fp4(const void* q, int64_t ld_q, const void* s, const float* global_scale, void* out, int64_t ld_out,
+                       int64_t rows, int64_t channels, uint32_t format, void* stream) {
+  const int st = sdq_validate_dequantize_fp4(q, ld_q, s, global_scale, out, ld_out, rows, channels, format);
+  if (st != SDQ_OK || rows == 0) return st;
+  int sms = 0;
+  if (const int e = sdq_internal::sm_count(&sms)) return e;
+  sdq::fp4::DequantParams p = {};
+  p.q = static_cast<const uint8_t*>(q);
+  p.s = static_cast<const uint8_t*>(s);
+  p.global = global_scale;
+  p.out = static_cast<uint8_t*>(out);
+  p.rows = rows;
+  p.ld_q = ld_q;
+  p.ld_out = ld_out;
+  p.channels = static_cast<int32_t>(channels);
+  p.tiles_k = static_cast<int32_t>(tiles_of(channels, format));
+  const int64_t need = (rows * (channels / 8) + sdq::fp4::kThreads - 1) / sdq::fp4::kThreads;
+  void* args[] = {&p};
+  return launch(format & SDQ_FMT_E8M0 ? reinterpret_cast<const void*>(sdq::fp4::dequantize_kernel<Scales::kE8M0>)
+                                      : reinterpret_cast<const void*>(sdq::fp4::dequantize_kernel<Scales::kE4M3>),
+                static_cast<unsigned>(std::min<int64_t>(need, int64_t{sms} * 8)), sdq::fp4::kThreads, 0,
+                static_cast<cudaStream_t>(stream), args);
+}
+
+int sdq_validate_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_global, const void* b,
+                            int64_t ld_b, const void* b_s, const float* b_global, const void* out, int64_t ld_out,
+                            int64_t m, int64_t n, int64_t k, uint32_t format) {
+  if (!format_ok(format, SDQ_FMT_OUT_F32)) return SDQ_ERR_FORMAT;
+  if (m < 0 || m > SDQ_MAX_M || n < 0 || n > SDQ_MAX_M || !length_ok(k)) return SDQ_ERR_SHAPE;
+  if ((m + 127) / 128 * ((n + 127) / 128) > INT32_MAX) return SDQ_ERR_SHAPE;
+  if (m == 0 || n == 0) return SDQ_OK;
+  if (!a || !a_s || !b || !b_s || !out) return SDQ_ERR_NULL;
+  if (ld_a < k / 2 || ld_a > SDQ_MAX_LD || ld_b < k / 2 || ld_b > SDQ_MAX_LD || ld_out < n || ld_out > SDQ_MAX_LD)
+    return SDQ_ERR_STRIDE;
+  if (misaligned(a, 15) || (ld_a & 15) || misaligned(b, 15) || (ld_b & 15) || misaligned(a_s, 15) ||
+      misaligned(b_s, 15) || misaligned(a_global, 3) || misaligned(b_global, 3) ||
+      misaligned(out, format & SDQ_FMT_OUT_F32 ? 3 : 1))
+    return SDQ_ERR_ALIGN;
+  return SDQ_OK;
+}
+
+int sdq_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_global, const void* b, int64_t ld_b,
+                   const void* b_s, const float* b_global, void* out, int64_t ld_out, int64_t m, int64_t n, int64_t k,
+                   uint32_t format, void* stream) {
+  const int st = sdq_validate_matmul_fp4(a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format);
+  if (st != SDQ_OK || m == 0 || n == 0) return st;
+  // Up to 128 rows of a: they are the columns of the accumulator, as few as
+  // hold them, and the weights' rows are its lanes.
+  const bool swapped = m <= 128;
+  sdq::mm4::Params p = {};
+  p.sa = static_cast<const uint8_t*>(swapped ? b_s : a_s);
+  p.sb = static_cast<const uint8_t*>(swapped ? a_s : b_s);
+  p.ga = a_global;
+  p.gb = b_global;
+  p.out = static_cast<uint8_t*>(out);
+  p.ld_out = ld_out;
+  p.rows_a = swapped ? n : m;
+  p.rows_b = swapped ? m : n;
+  p.codes = static_cast<int32_t>(k);
+  p.tiles_k = static_cast<int32_t>(tiles_of(k, format));
+  p.swapped = swapped;
+  p.out_f32 = format & SDQ_FMT_OUT_F32 ? 1 : 0;
+  p.wait_limit_ns = sdq_internal::wait_limit();
+  const MatmulKernel kern = format & SDQ_FMT_E8M0 ? matmul_for<Scales::kE8M0>(p.rows_b) : matmul_for<Scales::kE4M3>(p.rows_b);
+  if (const int e = sdq_internal::device_status_word(&p.status)) return e;
+  CUtensorMap ma, mb;
+  if (const int e = sdq_internal::make_code_map(&ma, swapped ? b : a, k / 2, p.rows_a, swapped ? ld_b : ld_a, 128)) return e;
+  if (const int e = sdq_internal::make_code_map(&mb, swapped ? a : b, k / 2, p.rows_b, swapped ? ld_a : ld_b, kern.n)) return e;
+  const cudaError_t e = cudaFuncSetAttribute(kern.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kern.smem));
+  if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
+  p.grid_a = static_cast<int32_t>((p.rows_a + 127) / 128);
+  const int64_t grid = p.grid_a * ((p.rows_b + kern.n - 1) / kern.n);
+  void* args[] = {&ma, &mb, &p};
+  return launch(kern.fn, static_cast<unsigned>(grid), sdq::mm4::kThreads, kern.smem, static_cast<cudaStream_t>(stream), args);
+}
+
+}  // extern "C"

@@ -1,0 +1,323 @@
+// The product of two microscaled 4-bit operands, C = A B^T, on the tensor cores.
+//
+//   C[m, n] = alpha * sum_k (a[m, k] sa[m, k / G]) (b[n, k] sb[n, k / G])
+//
+// E2M1 codes two to a byte, G = 32 with E8M0 scales or G = 16 with E4M3
+// scales, fp32 sums in tensor memory, alpha = the product of the two scales
+// per tensor.  tcgen05.mma applies the block scales itself: it reads them
+// from tensor memory, where tcgen05.cp puts the 512-byte scale tiles as they
+// lie in memory (128 rows x 4 groups).
+//
+// One side of the product has 128 rows a CTA (the accumulator's lanes), the
+// other kN (its columns).
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "quant_common.cuh"
+
+namespace sdq {
+namespace mm4 {
+
+using quant::Scales;
+
+constexpr int kRows = 128;                  // lanes of the accumulator
+constexpr int kStepBytes = 128;             // bytes of a row a stage holds: 256 codes
+constexpr int kStepCodes = 2 * kStepBytes;
+constexpr int kMmaCodes = 64;               // codes one tcgen05.mma takes along k
+constexpr int kMmas = kStepCodes / kMmaCodes;
+constexpr int kThreads = 192;               // a load warp, an mma warp, four epilogue warps
+
+struct Params {
+  const uint8_t* sa;       // scale tiles of the side with 128 rows a CTA
+  const uint8_t* sb;       // of the other side
+  const float* ga;         // scales per tensor, or null
+  const float* gb;
+  uint8_t* out;
+  int64_t ld_out;          // elements
+  int64_t rows_a, rows_b;  // rows of the two sides
+  int32_t codes;           // k
+  int32_t tiles_k;         // scale tiles along k
+  int32_t grid_a;          // CTAs along the side with 128 rows each
+  int32_t swapped;         // out is [rows_b, rows_a] instead of [rows_a, rows_b]
+  int32_t out_f32;         // fp32 elements instead of bf16
+  int* status;
+  uint64_t wait_limit_ns;
+};
+
+template <Scales S, int kN>
+struct Shape {
+  static constexpr int kScaleTiles = S == Scales::kE8M0 ? 2 : 4;   // scale tiles a stage holds per 128 rows
+  static constexpr int kBlocksB = kN > 128 ? 2 : 1;                // 128-row blocks of the other side
+  static constexpr int kCodesA = kRows * kStepBytes;
+  static constexpr int kCodesB = kN * kStepBytes;
+  static constexpr int kScaleA = kScaleTiles * 512;
+  static constexpr int kScaleB = kBlocksB * kScaleTiles * 512;
+  static constexpr int kStage = kCodesA + kCodesB + kScaleA + kScaleB;   // a multiple of 1024
+  static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
+  // tensor memory: the sums, then two sets of scales used in turn
+  static constexpr int kColsScaleA = kScaleTiles * 4;
+  static constexpr int kColsScaleB = kScaleTiles * 4 * kBlocksB;
+  static constexpr int kColsScale = kColsScaleA + kColsScaleB;
+  static constexpr int kColsSum = kN < 32 ? 32 : kN;
+  static constexpr int kColsUsed = kColsSum + 2 * kColsScale;
+  static constexpr int kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
+  static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStage);
+  static_assert(kColsUsed <= 512, "tensor memory has 512 columns");
+  static_assert(kStage % 1024 == 0, "the swizzled boxes start on 1024 bytes");
+};
+
+// ---- tcgen05 -------------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Arrives on the barrier once all tcgen05 work this thread has issued is done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A scale tile from shared memory to 4 columns: 32 rows of 16 bytes, copied to
+// each quarter of the lanes.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <Scales S>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                    bool accumulate) {
+  if (S == Scales::kE8M0)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+// 32 columns of the warp's 32 lanes; the registers are valid after load_wait().
+__device__ __forceinline__ void load_sums32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Shared-memory descriptors (start address, strides in units of 16 bytes,
+// version 1): K-major rows of 128 swizzled bytes, eight rows every 1024; and
+// the scale tiles, unswizzled, eight rows of 16 bytes every 128.
+__device__ __forceinline__ uint64_t desc_codes(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (8ull << 32) | (1ull << 46);
+}
+
+// Instruction descriptor of the block-scaled 4-bit kinds: E2M1 operands
+// (format 1 at bits 7 and 10), n / 8 at bit 17, E8M0 scales at bit 23,
+// m / 128 at bit 27; the scale's first byte in its column word goes to bits 4
+// (B) and 29 (A).
+template <Scales S, int kN>
+__device__ __forceinline__ uint32_t instruction(uint32_t scale_byte) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kN / 8) << 17) | (S == Scales::kE8M0 ? 1u << 23 : 0u) |
+         (1u << 27) | (scale_byte << 4) | (scale_byte << 29);
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+// ---- waits ----------------------------------------------------------------------
+
+struct Sync {
+  int* status;         // the device status word
+  volatile int* abort; // shared: set by the first wait that runs out
+  uint64_t limit_ns;
+};
+
+// Waits for the barrier's phase, no longer than the limit; false once any
+// wait of the CTA has run out.
+__device__ __forceinline__ bool wait(const Sync& y, uint32_t bar, uint32_t parity) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*y.abort) return false;
+    if (globaltimer_ns() - t0 > y.limit_ns) {
+      *y.abort = 1;
+      atomicOr(y.status, 1);
+      return false;
+    }
+  }
+  return true;
+}
+
+// ---- the kernel -----------------------------------------------------------------
+
+__device__ __forceinline__ void store_out(const Params& p, int64_t row, int64_t col, float v) {
+  const int64_t at = row * p.ld_out + col;
+  if (p.out_f32)
+    reinterpret_cast<float*>(p.out)[at] = v;
+  else
+    reinterpret_cast<uint16_t*>(p.out)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+}
+
+template <Scales S, int kN>
+__global__ void __launch_bounds__(kThreads, 1)
+    matmul_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const Params p) {
+  using Z = Shape<S, kN>;
+  extern __shared__ uint8_t raw[];
+  __shared__ alignas(8) uint64_t bars[2 * Z::kStages + 1];
+  __shared__ uint32_t tmem_addr;
+  __shared__ int abort_flag, issued_flag;
+  const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * Z::kStages, done = empty + 8 * Z::kStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * Z::kStages + 1; ++i) mbar_init(full + 8 * i, 1);
+    fence_mbar_init();
+    abort_flag = 0;
+    issued_flag = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_addr), Z::kCols);
+    tmem_relinquish();
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  grid_dependency_wait();     // operands may come from the previous kernel in the stream
+  grid_launch_dependents();   // after the allocation: a later kernel's cannot come first
+  const uint32_t tmem = *const_cast<volatile uint32_t*>(&tmem_addr);
+  const Sync sync = {p.status, &abort_flag, p.wait_limit_ns};
+  const int steps = (p.codes + kStepCodes - 1) / kStepCodes;
+  const int tile_b = blockIdx.x / p.grid_a, tile_a = blockIdx.x - tile_b * p.grid_a;
+  const int64_t a0 = static_cast<int64_t>(tile_a) * kRows, b0 = static_cast<int64_t>(tile_b) * kN;
+  const int blocks_b = static_cast<int>(min(static_cast<int64_t>(Z::kBlocksB), (p.rows_b - b0 + 127) / 128));
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < steps; ++i) {
+        const int st = i % Z::kStages;
+        if (i >= Z::kStages && !wait(sync, empty + 8 * st, ((i / Z::kStages) - 1) & 1)) break;
+        const uint32_t buf = ring + st * Z::kStage, bar = full + 8 * st;
+        const int k_tile = i * Z::kScaleTiles;
+        const int tiles = min(Z::kScaleTiles, p.tiles_k - k_tile);
+        mbar_arrive_expect_tx(bar, Z::kCodesA + Z::kCodesB + (1 + blocks_b) * tiles * 512);
+        tma_load(buf, &ma, bar, i * kStepBytes, static_cast<int32_t>(a0));
+        tma_load(buf + Z::kCodesA, &mb, bar, i * kStepBytes, static_cast<int32_t>(b0));
+        const uint32_t sc = buf + Z::kCodesA + Z::kCodesB;
+        bulk_load(sc, p.sa + ((a0 >> 7) * p.tiles_k + k_tile) * 512, tiles * 512, bar);
+        for (int b = 0; b < blocks_b; ++b)
+          bulk_load(sc + Z::kScaleA + b * Z::kScaleTiles * 512, p.sb + (((b0 >> 7) + b) * p.tiles_k + k_tile) * 512,
+                    tiles * 512, bar);
+        issued_flag = i + 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0; i < steps && ok; ++i) {
+        const int st = i % Z::kStages;
+        ok = wait(sync, full + 8 * st, (i / Z::kStages) & 1);
+        if (!ok) break;
+        fence_after();
+        const uint32_t buf = ring + st * Z::kStage;
+        const uint32_t sc = buf + Z::kCodesA + Z::kCodesB;
+        const uint32_t ta = tmem + Z::kColsSum + (i & 1) * Z::kColsScale, tb = ta + Z::kColsScaleA;
+#pragma unroll
+        for (int j = 0; j < Z::kScaleTiles; ++j) {
+          copy_scales(ta + 4 * j, desc_scales(sc + j * 512));
+#pragma unroll
+          for (int b = 0; b < Z::kBlocksB; ++b)
+            copy_scales(tb + 4 * (j * Z::kBlocksB + b), desc_scales(sc + Z::kScaleA + (b * Z::kScaleTiles + j) * 512));
+        }
+        const int mmas = min(kMmas, (p.codes - i * kStepCodes + kMmaCodes - 1) / kMmaCodes);
+        for (int j = 0; j < mmas; ++j) {
+          const int tile = S == Scales::kE8M0 ? j >> 1 : j;
+          mma<S>(tmem, desc_codes(buf + 32 * j), desc_codes(buf + Z::kCodesA + 32 * j),
+                 instruction<S, kN>(S == Scales::kE8M0 ? 2 * (j & 1) : 0), ta + 4 * tile, tb + 4 * tile * Z::kBlocksB,
+                 i > 0 || j > 0);
+        }
+        commit(empty + 8 * st);
+      }
+      commit(done);
+      mbar_wait(done, 0, sync.limit_ns);   // nothing of the tensor cores is in flight when the CTA frees its memory
+    }
+  } else {
+    const bool ok = wait(sync, done, 0);
+    fence_after();
+    if (ok && !*sync.abort) {
+      const int quarter = warp & 3;   // the lanes a warp may read
+      const int64_t ra = a0 + quarter * 32 + lane;
+      const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f);
+#pragma unroll 1
+      for (int c = 0; c < kN; c += 32) {
+        if (b0 + c >= p.rows_b) break;
+        uint32_t r[32];
+        load_sums32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, r);
+        load_wait();
+        if (ra < p.rows_a) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int64_t rb = b0 + c + e;
+            if (c + e < kN && rb < p.rows_b) {
+              const float v = __uint_as_float(r[e]) * alpha;
+              if (p.swapped)
+                store_out(p, rb, ra, v);
+              else
+                store_out(p, ra, rb, v);
+            }
+          }
+        }
+      }
+    }
+    fence_before();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_flag) {   // copies still in flight write this CTA's shared memory
+    for (int i = max(0, issued_flag - Z::kStages); i < issued_flag; ++i)
+      mbar_wait(full + 8 * (i % Z::kStages), (i / Z::kStages) & 1, sync.limit_ns);
+  }
+  __syncthreads();
+  __syncwarp();
+  if (warp == 1) {
+    fence_after();
+    tmem_free(tmem, Z::kCols);
+  }
+}
+
+}  // namespace mm4
+}  // namespace sdq

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "sdq.h"
+#include "sdq_internal.h"
 #include "sdq_kernel.cuh"
 #include "sdq_kernel256.cuh"
 
@@ -115,7 +116,7 @@ int cuda_fail(cudaError_t e) {
 
 }  // namespace
 
-// Shared with the library's other translation units (fwd_api.cu).
+// Shared with the library's other translation units.
 namespace sdq_internal {
 int cuda_fail(cudaError_t e) { return ::cuda_fail(e); }
 }  // namespace sdq_internal
@@ -201,6 +202,72 @@ int make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
   if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
   return SDQ_OK;
 }
+
+}  // namespace
+
+// Shared with the library's other translation units (sdq_internal.h).
+namespace sdq_internal {
+
+uint64_t wait_limit() { return ::wait_limit_ns(); }
+
+namespace {
+struct DeviceFacts {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+  int sms = 0;
+  int* word = nullptr;
+};
+DeviceFacts g_facts[kMaxDevices];
+
+int facts(DeviceFacts** out) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return ::cuda_fail(e);
+  if (dev < 0 || dev >= kMaxDevices) return ::cuda_fail(cudaErrorInvalidDevice);
+  DeviceFacts& f = g_facts[dev];
+  std::call_once(f.once, [&f, dev] {
+    f.err = cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev);
+    void* word = nullptr;
+    if (f.err == cudaSuccess) f.err = cudaGetSymbolAddress(&word, sdq::g_sdq_dev_status);
+    f.word = static_cast<int*>(word);
+  });
+  if (f.err != cudaSuccess) return ::cuda_fail(f.err);
+  *out = &f;
+  return SDQ_OK;
+}
+}  // namespace
+
+int sm_count(int* sms) {
+  DeviceFacts* f = nullptr;
+  const int st = facts(&f);
+  if (st == SDQ_OK) *sms = f->sms;
+  return st;
+}
+
+int device_status_word(int** word) {
+  DeviceFacts* f = nullptr;
+  const int st = facts(&f);
+  if (st == SDQ_OK) *word = f->word;
+  return st;
+}
+
+int make_code_map(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows, uint64_t row_bytes,
+                  uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return ::cuda_fail(cudaErrorNotSupported);
+  const cuuint64_t dims[2] = {inner_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SDQ_OK : ::cuda_fail(cudaErrorInvalidValue);
+}
+
+}  // namespace sdq_internal
+
+namespace {
 
 // One call's arrays and leading dimensions (elements from one row to the
 // next), as sdq_fuse_strided takes them.
