@@ -8,6 +8,7 @@
 
 #include "fp4_kernel.cuh"
 #include "fp4_matmul.cuh"
+#include "fp4_matmul_pair.cuh"
 #include "sdq.h"
 #include "sdq_internal.h"
 
@@ -59,6 +60,51 @@ struct MatmulKernel {
 template <Scales S, int kN>
 MatmulKernel matmul_of() {
   return {reinterpret_cast<const void*>(sdq::mm4::matmul_kernel<S, kN>), sdq::mm4::Shape<S, kN>::kSmem, kN};
+}
+
+template <Scales S, int kN>
+MatmulKernel pair_of() {
+  return {reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kN>), sdq::mm4::PairShape<S, kN>::kSmem, kN};
+}
+
+// One call of the product, checked.
+struct Product {
+  const void* a; int64_t ld_a; const void* a_s; const float* a_global;
+  const void* b; int64_t ld_b; const void* b_s; const float* b_global;
+  void* out; int64_t ld_out;
+  int64_t m, n, k;
+  uint32_t format;
+  cudaStream_t stream;
+};
+
+int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
+  const int64_t tiles_k = tiles_of(c.k, c.format);
+  sdq::mm4::PairParams p = {};
+  p.ga = c.a_global;
+  p.gb = c.b_global;
+  p.out = static_cast<uint8_t*>(c.out);
+  p.ld_out = c.ld_out;
+  p.rows_a = c.m;
+  p.rows_b = c.n;
+  p.codes = static_cast<int32_t>(c.k);
+  p.tiles_a = static_cast<int32_t>((c.m + 255) / 256);
+  p.tiles_b = static_cast<int32_t>((c.n + kern.n - 1) / kern.n);
+  p.out_f32 = c.format & SDQ_FMT_OUT_F32 ? 1 : 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(c.out) | static_cast<uintptr_t>(c.ld_out * (p.out_f32 ? 4 : 2));
+  p.vec = at & 31 ? at & 15 ? 0 : 16 : 32;
+  p.wait_limit_ns = sdq_internal::wait_limit();
+  if (const int e = sdq_internal::device_status_word(&p.status)) return e;
+  CUtensorMap ma, mb, msa, msb;
+  const uint32_t stage = c.format & SDQ_FMT_E8M0 ? 2 : 4;   // scale tiles a stage
+  if (const int e = sdq_internal::make_code_map(&ma, c.a, c.k / 2, c.m, c.ld_a, 128)) return e;
+  if (const int e = sdq_internal::make_code_map(&mb, c.b, c.k / 2, c.n, c.ld_b, kern.n / 2)) return e;
+  if (const int e = sdq_internal::make_scale_map(&msa, c.a_s, tiles_k, (c.m + 127) / 128, stage)) return e;
+  if (const int e = sdq_internal::make_scale_map(&msb, c.b_s, tiles_k, (c.n + 127) / 128, stage)) return e;
+  const cudaError_t e = cudaFuncSetAttribute(kern.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kern.smem));
+  if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
+  const int64_t pairs = std::min<int64_t>(sms / 2, int64_t{p.tiles_a} * p.tiles_b);
+  void* args[] = {&ma, &mb, &msa, &msb, &p};
+  return launch(kern.fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kThreads, kern.smem, c.stream, args);
 }
 
 template <Scales S>
@@ -178,6 +224,12 @@ int sdq_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_
                    uint32_t format, void* stream) {
   const int st = sdq_validate_matmul_fp4(a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format);
   if (st != SDQ_OK || m == 0 || n == 0) return st;
+  int sms = 0;
+  if (const int e = sdq_internal::sm_count(&sms)) return e;
+  if (m > 128) {
+    const Product c = {a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format, static_cast<cudaStream_t>(stream)};
+    return launch_pair(c, format & SDQ_FMT_E8M0 ? pair_of<Scales::kE8M0, 256>() : pair_of<Scales::kE4M3, 256>(), sms);
+  }
   // Up to 128 rows of a: they are the columns of the accumulator, as few as
   // hold them, and the weights' rows are its lanes.
   const bool swapped = m <= 128;

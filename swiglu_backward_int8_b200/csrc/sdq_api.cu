@@ -265,6 +265,19 @@ int make_code_map(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint
   return r == CUDA_SUCCESS ? SDQ_OK : ::cuda_fail(cudaErrorInvalidValue);
 }
 
+int make_scale_map(CUtensorMap* map, const void* base, uint64_t tiles_k, uint64_t blocks, uint32_t box_tiles) {
+  auto fn = encode_fn();
+  if (!fn) return ::cuda_fail(cudaErrorNotSupported);
+  const cuuint64_t dims[2] = {tiles_k * 64, blocks};
+  const cuuint64_t strides[1] = {tiles_k * 512};
+  const cuuint32_t box[2] = {box_tiles * 64, 1};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SDQ_OK : ::cuda_fail(cudaErrorInvalidValue);
+}
+
 }  // namespace sdq_internal
 
 namespace {

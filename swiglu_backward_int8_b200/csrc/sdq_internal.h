@@ -26,4 +26,9 @@ uint64_t wait_limit();
 int make_code_map(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows, uint64_t row_bytes,
                   uint32_t box_rows);
 
+// Scale tiles of 512 bytes, `tiles_k` of them side by side for each of `blocks`
+// blocks of 128 rows, read `box_tiles` at a time (coordinates in words of 8
+// bytes); tiles out of range read as zero (sdq_api.cu).
+int make_scale_map(CUtensorMap* map, const void* base, uint64_t tiles_k, uint64_t blocks, uint32_t box_tiles);
+
 }  // namespace sdq_internal
