@@ -69,6 +69,15 @@ struct Shape {
   static_assert(kStage % 1024 == 0, "the swizzled boxes start on 1024 bytes");
 };
 
+// True in one lane of a converged warp.  A branch on it, unlike one on the lane's
+// number, lets the compiler keep the descriptors of the tensor-core
+// instructions in uniform registers: issuing them costs a third less.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 // ---- tcgen05 -------------------------------------------------------------------
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
@@ -171,7 +180,10 @@ struct Sync {
 // Waits for the barrier's phase, no longer than the limit; false once any
 // wait of the CTA has run out.
 __device__ __forceinline__ bool wait(const Sync& y, uint32_t bar, uint32_t parity) {
-  if (mbar_test_wait(bar, parity)) return true;
+  // (a try_wait suspends the thread for a while by itself; the timer, slow to
+  // read, comes in only once several have run out)
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (*y.abort) return false;
@@ -228,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int blocks_b = static_cast<int>(min(static_cast<int64_t>(Z::kBlocksB), (p.rows_b - b0 + 127) / 128));
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       for (int i = 0; i < steps; ++i) {
         const int st = i % Z::kStages;
         if (i >= Z::kStages && !wait(sync, empty + 8 * st, ((i / Z::kStages) - 1) & 1)) break;
@@ -247,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       for (int i = 0; i < steps && ok; ++i) {
         const int st = i % Z::kStages;
@@ -255,21 +267,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after();
         const uint32_t buf = ring + st * Z::kStage;
-        const uint32_t sc = buf + Z::kCodesA + Z::kCodesB;
         const uint32_t ta = tmem + Z::kColsSum + (i & 1) * Z::kColsScale, tb = ta + Z::kColsScaleA;
+        const uint64_t ds = desc_scales(buf + Z::kCodesA + Z::kCodesB);
 #pragma unroll
         for (int j = 0; j < Z::kScaleTiles; ++j) {
-          copy_scales(ta + 4 * j, desc_scales(sc + j * 512));
+          copy_scales(ta + 4 * j, ds + 32 * j);
 #pragma unroll
           for (int b = 0; b < Z::kBlocksB; ++b)
-            copy_scales(tb + 4 * (j * Z::kBlocksB + b), desc_scales(sc + Z::kScaleA + (b * Z::kScaleTiles + j) * 512));
+            copy_scales(tb + 4 * (j * Z::kBlocksB + b), ds + (Z::kScaleA >> 4) + 32 * (b * Z::kScaleTiles + j));
         }
+        const uint64_t da = desc_codes(buf), db = desc_codes(buf + Z::kCodesA);
         const int mmas = min(kMmas, (p.codes - i * kStepCodes + kMmaCodes - 1) / kMmaCodes);
-        for (int j = 0; j < mmas; ++j) {
-          const int tile = S == Scales::kE8M0 ? j >> 1 : j;
-          mma<S>(tmem, desc_codes(buf + 32 * j), desc_codes(buf + Z::kCodesA + 32 * j),
-                 instruction<S, kN>(S == Scales::kE8M0 ? 2 * (j & 1) : 0), ta + 4 * tile, tb + 4 * tile * Z::kBlocksB,
-                 i > 0 || j > 0);
+#pragma unroll
+        for (int j = 0; j < kMmas; ++j) {
+          constexpr int kPerTile = S == Scales::kE8M0 ? 2 : 1;   // products a scale tile lasts
+          if (j < mmas)
+            mma<S>(tmem, da + 2 * j, db + 2 * j, instruction<S, kN>(S == Scales::kE8M0 ? 2 * (j & 1) : 0),
+                   ta + 4 * (j / kPerTile), tb + 4 * (j / kPerTile) * Z::kBlocksB, i > 0 || j > 0);
         }
         commit(empty + 8 * st);
       }

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int tiles = p.tiles_a * p.tiles_b, first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t full0 = at_rank(full, 0);
       int n = 0;   // loads so far
       bool ok = true;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           ok = wait(sync, empty + 8 * (i % Z::kStages), (i / Z::kStages) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       const uint32_t empty1 = at_rank(empty, 1), sums1 = at_rank(sums, 1);
       int n = 0, k = 0;   // loads, tiles so far
       bool ok = true;
@@ -253,21 +253,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (!ok) break;
           fence_after();
           const uint32_t buf = ring + st * Z::kStage;
-          const uint32_t sc = buf + Z::kCodesA + Z::kCodesB;
           const uint32_t ca = tmem + Z::kScaleCol + (n & 1) * Z::kColsScale, cb = ca + Z::kColsScaleA;
+          const uint64_t ds = desc_scales(buf + Z::kCodesA + Z::kCodesB);
 #pragma unroll
           for (int j = 0; j < Z::kScaleTiles; ++j) {
-            copy_scales_pair(ca + 4 * j, desc_scales(sc + j * 512));
+            copy_scales_pair(ca + 4 * j, ds + 32 * j);
 #pragma unroll
             for (int b = 0; b < Z::kBlocksB; ++b)
-              copy_scales_pair(cb + 4 * (j * Z::kBlocksB + b), desc_scales(sc + Z::kScaleA + (b * Z::kScaleTiles + j) * 512));
+              copy_scales_pair(cb + 4 * (j * Z::kBlocksB + b), ds + (Z::kScaleA >> 4) + 32 * (b * Z::kScaleTiles + j));
           }
+          const uint64_t da = desc_codes(buf), db = desc_codes(buf + Z::kCodesA);
           const int mmas = min(kMmas, (p.codes - i * kStepCodes + kMmaCodes - 1) / kMmaCodes);
-          for (int j = 0; j < mmas; ++j) {
-            const int tile = S == Scales::kE8M0 ? j >> 1 : j;
-            mma_pair<S>(acc, desc_codes(buf + 32 * j), desc_codes(buf + Z::kCodesA + 32 * j),
-                        instruction_pair<S, kN>(S == Scales::kE8M0 ? 2 * (j & 1) : 0), ca + 4 * tile,
-                        cb + 4 * tile * Z::kBlocksB, i > 0 || j > 0);
+#pragma unroll
+          for (int j = 0; j < kMmas; ++j) {
+            constexpr int kPerTile = S == Scales::kE8M0 ? 2 : 1;   // products a scale tile lasts
+            if (j < mmas)
+              mma_pair<S>(acc, da + 2 * j, db + 2 * j, instruction_pair<S, kN>(S == Scales::kE8M0 ? 2 * (j & 1) : 0),
+                          ca + 4 * (j / kPerTile), cb + 4 * (j / kPerTile) * Z::kBlocksB, i > 0 || j > 0);
           }
           commit_pair(empty + 8 * st);
           commit_pair(empty1 + 8 * st);
