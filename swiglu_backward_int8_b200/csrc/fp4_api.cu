@@ -91,19 +91,21 @@ int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
   p.tiles_b = static_cast<int32_t>((c.n + kern.n - 1) / kern.n);
   p.out_f32 = c.format & SDQ_FMT_OUT_F32 ? 1 : 0;
   const uintptr_t at = reinterpret_cast<uintptr_t>(c.out) | static_cast<uintptr_t>(c.ld_out * (p.out_f32 ? 4 : 2));
-  p.vec = at & 31 ? at & 15 ? 0 : 16 : 32;
+  p.vec = at & 15 ? 0 : 1;
   p.wait_limit_ns = sdq_internal::wait_limit();
   if (const int e = sdq_internal::device_status_word(&p.status)) return e;
-  CUtensorMap ma, mb, msa, msb;
+  CUtensorMap ma, mb, msa, msb, mo = {};
   const uint32_t stage = c.format & SDQ_FMT_E8M0 ? 2 : 4;   // scale tiles a stage
   if (const int e = sdq_internal::make_code_map(&ma, c.a, c.k / 2, c.m, c.ld_a, 128)) return e;
   if (const int e = sdq_internal::make_code_map(&mb, c.b, c.k / 2, c.n, c.ld_b, kern.n / 2)) return e;
   if (const int e = sdq_internal::make_scale_map(&msa, c.a_s, tiles_k, (c.m + 127) / 128, stage)) return e;
   if (const int e = sdq_internal::make_scale_map(&msb, c.b_s, tiles_k, (c.n + 127) / 128, stage)) return e;
+  if (p.vec)
+    if (const int e = sdq_internal::make_out_map(&mo, c.out, p.out_f32, c.n, c.m, c.ld_out)) return e;
   const cudaError_t e = cudaFuncSetAttribute(kern.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kern.smem));
   if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
   const int64_t pairs = std::min<int64_t>(sms / 2, int64_t{p.tiles_a} * p.tiles_b);
-  void* args[] = {&ma, &mb, &msa, &msb, &p};
+  void* args[] = {&ma, &mb, &msa, &msb, &mo, &p};
   return launch(kern.fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kThreads, kern.smem, c.stream, args);
 }
 

@@ -251,31 +251,34 @@ int device_status_word(int** word) {
   return st;
 }
 
-int make_code_map(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows, uint64_t row_bytes,
-                  uint32_t box_rows) {
+// A 2-D tensor map; the encoder's checks are the descriptor's own.
+static int encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows,
+                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
   auto fn = encode_fn();
   if (!fn) return ::cuda_fail(cudaErrorNotSupported);
-  const cuuint64_t dims[2] = {inner_bytes, rows};
+  const cuuint64_t dims[2] = {inner, rows};
   const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t box[2] = {box_inner, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SDQ_OK : ::cuda_fail(cudaErrorInvalidValue);
 }
 
+int make_code_map(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows, uint64_t row_bytes,
+                  uint32_t box_rows) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner_bytes, rows, row_bytes, 128, box_rows,
+                CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 int make_scale_map(CUtensorMap* map, const void* base, uint64_t tiles_k, uint64_t blocks, uint32_t box_tiles) {
-  auto fn = encode_fn();
-  if (!fn) return ::cuda_fail(cudaErrorNotSupported);
-  const cuuint64_t dims[2] = {tiles_k * 64, blocks};
-  const cuuint64_t strides[1] = {tiles_k * 512};
-  const cuuint32_t box[2] = {box_tiles * 64, 1};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? SDQ_OK : ::cuda_fail(cudaErrorInvalidValue);
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_INT64, base, tiles_k * 64, blocks, tiles_k * 512, box_tiles * 64, 1,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+int make_out_map(CUtensorMap* map, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t ld) {
+  return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows,
+                ld * (f32 ? 4 : 2), f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace sdq_internal

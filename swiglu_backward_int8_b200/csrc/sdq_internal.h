@@ -31,4 +31,9 @@ int make_code_map(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint
 // bytes); tiles out of range read as zero (sdq_api.cu).
 int make_scale_map(CUtensorMap* map, const void* base, uint64_t tiles_k, uint64_t blocks, uint32_t box_tiles);
 
+// A row-major [rows, cols] array of fp32 or bf16, written in boxes of 32 rows x
+// 128 bytes with the 128-byte swizzle; what is out of range is not written
+// (sdq_api.cu).
+int make_out_map(CUtensorMap* map, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t ld);
+
 }  // namespace sdq_internal
