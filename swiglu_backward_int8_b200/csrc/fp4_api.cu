@@ -63,8 +63,10 @@ MatmulKernel matmul_of() {
 }
 
 template <Scales S, int kN>
-MatmulKernel pair_of() {
-  return {reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kN>), sdq::mm4::PairShape<S, kN>::kSmem, kN};
+MatmulKernel pair_of(bool f32) {
+  return {f32 ? reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kN, true>)
+              : reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kN, false>),
+          sdq::mm4::PairShape<S, kN>::kSmem, kN};
 }
 
 // One call of the product, checked.
@@ -89,8 +91,8 @@ int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
   p.codes = static_cast<int32_t>(c.k);
   p.tiles_a = static_cast<int32_t>((c.m + 255) / 256);
   p.tiles_b = static_cast<int32_t>((c.n + kern.n - 1) / kern.n);
-  p.out_f32 = c.format & SDQ_FMT_OUT_F32 ? 1 : 0;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(c.out) | static_cast<uintptr_t>(c.ld_out * (p.out_f32 ? 4 : 2));
+  const bool f32 = c.format & SDQ_FMT_OUT_F32;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(c.out) | static_cast<uintptr_t>(c.ld_out * (f32 ? 4 : 2));
   p.vec = at & 15 ? 0 : 1;
   p.wait_limit_ns = sdq_internal::wait_limit();
   if (const int e = sdq_internal::device_status_word(&p.status)) return e;
@@ -101,12 +103,12 @@ int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
   if (const int e = sdq_internal::make_scale_map(&msa, c.a_s, tiles_k, (c.m + 127) / 128, stage)) return e;
   if (const int e = sdq_internal::make_scale_map(&msb, c.b_s, tiles_k, (c.n + 127) / 128, stage)) return e;
   if (p.vec)
-    if (const int e = sdq_internal::make_out_map(&mo, c.out, p.out_f32, c.n, c.m, c.ld_out)) return e;
+    if (const int e = sdq_internal::make_out_map(&mo, c.out, f32, c.n, c.m, c.ld_out)) return e;
   const cudaError_t e = cudaFuncSetAttribute(kern.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kern.smem));
   if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
   const int64_t pairs = std::min<int64_t>(sms / 2, int64_t{p.tiles_a} * p.tiles_b);
   void* args[] = {&ma, &mb, &msa, &msb, &mo, &p};
-  return launch(kern.fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kThreads, kern.smem, c.stream, args);
+  return launch(kern.fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kPairThreads, kern.smem, c.stream, args);
 }
 
 template <Scales S>
@@ -230,7 +232,8 @@ int sdq_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_
   if (const int e = sdq_internal::sm_count(&sms)) return e;
   if (m > 128) {
     const Product c = {a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format, static_cast<cudaStream_t>(stream)};
-    return launch_pair(c, format & SDQ_FMT_E8M0 ? pair_of<Scales::kE8M0, 256>() : pair_of<Scales::kE4M3, 256>(), sms);
+    return launch_pair(c, format & SDQ_FMT_E8M0 ? pair_of<Scales::kE8M0, 256>(format & SDQ_FMT_OUT_F32)
+                                                 : pair_of<Scales::kE4M3, 256>(format & SDQ_FMT_OUT_F32), sms);
   }
   // Up to 128 rows of a: they are the columns of the accumulator, as few as
   // hold them, and the weights' rows are its lanes.

@@ -19,6 +19,9 @@
 namespace sdq {
 namespace mm4 {
 
+constexpr int kEpilogueWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kEpilogueWarps;   // a load warp, an mma warp, the epilogue's
+
 template <Scales S, int kN>
 struct PairShape {
   static constexpr int kScaleTiles = S == Scales::kE8M0 ? 2 : 4;   // a stage's scale tiles per 128 rows
@@ -28,7 +31,7 @@ struct PairShape {
   static constexpr int kScaleA = kScaleTiles * 512;
   static constexpr int kScaleB = kBlocksB * kScaleTiles * 512;
   static constexpr int kStage = kCodesA + kCodesB + kScaleA + kScaleB;
-  static constexpr int kBoxes = 4 * 2 * 32 * 128;   // two boxes of output an epilogue warp
+  static constexpr int kBoxes = kEpilogueWarps * 32 * 128;   // a box of output an epilogue warp
   static constexpr int kStages = (226 * 1024 - 1024 - kBoxes) / kStage > 8 ? 8 : (226 * 1024 - 1024 - kBoxes) / kStage;
   static constexpr int kColsScaleA = kScaleTiles * 4;
   static constexpr int kColsScale = kColsScaleA + kScaleTiles * 4 * kBlocksB;
@@ -37,7 +40,8 @@ struct PairShape {
   static constexpr int kShared = kN - kAcc1;                                // columns both accumulators use
   static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStage) + kBoxes;
   static_assert(kStage % 1024 == 0, "the swizzled boxes start on 1024 bytes");
-  static_assert(kAcc1 >= 0 && kAcc1 % 64 == 0 && kShared % 64 == 0, "whole pieces of 64 columns");
+  static_assert(kAcc1 >= 0 && kAcc1 % 64 == 0 && kShared % 64 == 0 && kShared <= 128,
+                "whole pieces of 64 columns, those that are shared the first of a warp");
 };
 
 struct PairParams {
@@ -48,7 +52,6 @@ struct PairParams {
   int64_t rows_a, rows_b;
   int32_t codes;
   int32_t tiles_a, tiles_b;
-  int32_t out_f32;
   int32_t vec;             // the output's rows start on 16 bytes: bulk stores
   int* status;
   uint64_t wait_limit_ns;
@@ -157,7 +160,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const PairPara
     __syncwarp();
     if (lane == 0 && row0 < p.rows_a && col < p.rows_b)
       box_store(map, box, static_cast<int32_t>(col), static_cast<int32_t>(row0));
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // an empty one too: boxes are counted in groups
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   } else {
     __syncwarp();
     const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.rows_a - row0));
@@ -184,8 +187,8 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const PairPara
 
 // ---- the kernel -----------------------------------------------------------------------
 
-template <Scales S, int kN>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+template <Scales S, int kN, bool kF32>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     matmul_pair_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                        const __grid_constant__ CUtensorMap msa, const __grid_constant__ CUtensorMap msb,
                        const __grid_constant__ CUtensorMap mo, const PairParams p) {
@@ -203,10 +206,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t full = smem_u32(bars), empty = full + 8 * Z::kStages, sums = empty + 8 * Z::kStages, freed = sums + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
+  if (threadIdx.x == 32) {   // kernel parameters: no earlier kernel writes them
+    prefetch_tensormap(&ma);
+    prefetch_tensormap(&mb);
+    prefetch_tensormap(&msa);
+    prefetch_tensormap(&msb);
+    if (p.vec) prefetch_tensormap(&mo);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * Z::kStages + 2; ++i) mbar_init(full + 8 * i, 1);
-    mbar_init(freed, 8);
-    mbar_init(freed + 8, 8);
+    mbar_init(freed, 2 * kEpilogueWarps);
+    mbar_init(freed + 8, 2 * kEpilogueWarps);
     fence_mbar_init();
     abort_flag = 0;
   }
@@ -300,59 +310,49 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
     }
   } else {
+    // Two warps a quarter of the lanes take turns at the pieces of 64 columns.
+    // The columns that the next tile overwrites come first (the last ones of the
+    // first accumulator, the first ones of the second) and are given back once
+    // they are in registers: the tensor cores wait for them.
+    constexpr int kPieces = kN / 64;
     const uint32_t freed0 = at_rank(freed, 0);
-    const int quarter = warp & 3;   // the lanes a warp may read
+    const int quarter = warp & 3, half = (warp - 2) >> 2;   // the lanes a warp may read, and which of the two it is
     const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f);
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t boxes = ring + Z::kStages * Z::kStage + quarter * 2 * kBoxBytes;
-    int k = 0, nbox = 0;
-    for (int t = first; t < tiles; t += stride, ++k) {
-      if (!wait(sync, sums + 8 * (k & 1), (k >> 1) & 1)) break;
+    const uint32_t box = ring + Z::kStages * Z::kStage + (warp - 2) * kBoxBytes;
+    // The round before the first (k = -1) stores nothing: while the first tile is
+    // computed it brings this code into the instruction cache, which a launch
+    // finds cold (1100 cycles at the end of a call that has one tile).
+    for (int k = -1;; ++k) {
+      const int t = first + k * stride;
+      if (k >= 0 && (t >= tiles || !wait(sync, sums + 8 * (k & 1), (k >> 1) & 1))) break;
       fence_after();
       const int tb = t / p.tiles_a, ta = t - tb * p.tiles_a;
-      const int64_t row0 = static_cast<int64_t>(ta) * 256 + rank * 128 + quarter * 32;
+      const int64_t row0 = k < 0 ? p.rows_a : static_cast<int64_t>(ta) * 256 + rank * 128 + quarter * 32;
       const int64_t col0 = static_cast<int64_t>(tb) * kN;
-      const uint32_t acc = tmem + ((k & 1) ? Z::kAcc1 : 0) + lanes;
-      // The columns that the next tile overwrites come first (the last ones of
-      // the first accumulator, the first ones of the second), loaded together
-      // and given back before they are stored: the tensor cores wait for them.
-      constexpr int kPieces = kN / 64, kGroup = Z::kShared > 0 ? Z::kShared / 64 : 1;   // of 64 columns
+      const uint32_t acc = tmem + (k > 0 && (k & 1) ? Z::kAcc1 : 0) + lanes;
       const int start = Z::kShared > 0 && (k & 1) == 0 ? Z::kAcc1 / 64 : 0;
-#pragma unroll
-      for (int c = 0; c < kPieces; c += kGroup) {
-        uint32_t r[kGroup][64];
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          if (c + j < kPieces) {
-            const uint32_t at = acc + (start + c + j) % kPieces * 64;
-            load_sums32(at, *reinterpret_cast<uint32_t(*)[32]>(&r[j][0]));
-            load_sums32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[j][32]));
-          }
-        }
+      if (Z::kShared > 0 && k >= 0 && half >= Z::kShared / 64) {   // none of its pieces is shared: it is done with the tile before
+        __syncwarp();
+        if (lane == 0) arrive_at(freed0 + 8 * (k & 1));
+      }
+#pragma unroll 1
+      for (int c = half; c < (k < 0 ? half + 1 : kPieces); c += 2) {
+        const int piece = (start + c) % kPieces;
+        uint32_t r[64];
+        load_sums32(acc + piece * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+        load_sums32(acc + piece * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
         load_wait();
-        if (Z::kShared > 0 ? c == 0 : c + kGroup >= kPieces) {
+        if (k >= 0 && (Z::kShared > 0 ? c < Z::kShared / 64 : c + 2 >= kPieces)) {
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_at(freed0 + 8 * (k & 1));
         }
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          if (c + j < kPieces) {
-            const int64_t col = col0 + (start + c + j) % kPieces * 64;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {   // an fp32 piece is two boxes
-              if (h == 1 && !p.out_f32) break;
-              const uint32_t box = boxes + (nbox & 1) * kBoxBytes;
-              // the store before the last from this box has read it
-              asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-              __syncwarp();
-              if (p.out_f32)
-                store_box<true>(&mo, p, box, lane, &r[j][32 * h], alpha, row0, col + 32 * h);
-              else
-                store_box<false>(&mo, p, box, lane, &r[j][0], alpha, row0, col);
-              ++nbox;
-            }
-          }
+        for (int h = 0; h < (kF32 ? 2 : 1); ++h) {   // an fp32 piece is two boxes
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the store before has read the box
+          __syncwarp();
+          store_box<kF32>(&mo, p, box, lane, &r[32 * h], alpha, row0, col0 + piece * 64 + 32 * h);
         }
       }
     }
