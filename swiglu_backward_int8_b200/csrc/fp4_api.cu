@@ -29,17 +29,21 @@ int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int group_of(uint32_t f) { return f & SDQ_FMT_E8M0 ? 32 : 16; }
 int64_t tiles_of(int64_t k, uint32_t f) { return (k / group_of(f) + 3) / 4; }   // scale tiles along k
 
-int launch(const void* kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, void** args) {
+int launch(const void* kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, void** args,
+           unsigned cluster = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
   return e == cudaSuccess ? SDQ_OK : sdq_internal::cuda_fail(e);
 }
@@ -56,11 +60,6 @@ struct MatmulKernel {
   size_t smem;
   int n;
 };
-
-template <Scales S, int kN>
-MatmulKernel matmul_of() {
-  return {reinterpret_cast<const void*>(sdq::mm4::matmul_kernel<S, kN>), sdq::mm4::Shape<S, kN>::kSmem, kN};
-}
 
 template <Scales S, int kN>
 MatmulKernel pair_of(bool f32) {
@@ -111,10 +110,41 @@ int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
   return launch(kern.fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kPairThreads, kern.smem, c.stream, args);
 }
 
+// Few rows of a: clusters that share the steps along k.
 template <Scales S>
-MatmulKernel matmul_for(int64_t n) {
-  return n <= 16 ? matmul_of<S, 16>() : n <= 32 ? matmul_of<S, 32>() : n <= 64 ? matmul_of<S, 64>()
-       : n <= 128 ? matmul_of<S, 128>() : matmul_of<S, 256>();
+int launch_strip(const Product& c, int sms) {
+  using Z = sdq::mm4::StripShape<S>;
+  sdq::mm4::Params p = {};
+  p.sb = static_cast<const uint8_t*>(c.b_s);
+  p.sa = static_cast<const uint8_t*>(c.a_s);
+  p.ga = c.a_global;
+  p.gb = c.b_global;
+  p.out = static_cast<uint8_t*>(c.out);
+  p.ld_out = c.ld_out;
+  p.rows_a = c.m;
+  p.rows_b = c.n;
+  p.codes = static_cast<int32_t>(c.k);
+  p.tiles_k = static_cast<int32_t>(tiles_of(c.k, c.format));
+  p.cols = static_cast<int32_t>(std::min<int64_t>(128, up(c.m, 16)));
+  p.tiles_b = static_cast<int32_t>((c.n + 127) / 128);
+  p.stage = Z::stage(p.cols);
+  p.out_f32 = c.format & SDQ_FMT_OUT_F32 ? 1 : 0;
+  p.wait_limit_ns = sdq_internal::wait_limit();
+  if (const int e = sdq_internal::device_status_word(&p.status)) return e;
+  CUtensorMap ma, mb;
+  if (const int e = sdq_internal::make_code_map(&mb, c.b, c.k / 2, c.n, c.ld_b, 128)) return e;
+  if (const int e = sdq_internal::make_code_map(&ma, c.a, c.k / 2, c.m, c.ld_a, p.cols)) return e;
+  const void* fn = reinterpret_cast<const void*>(sdq::mm4::matmul_strip_kernel<S>);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 210 * 1024);
+  if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
+  const int64_t tiles = p.tiles_b * ((c.m + p.cols - 1) / p.cols);
+  const int64_t steps = (c.k + sdq::mm4::kStepCodes - 1) / sdq::mm4::kStepCodes;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= (p.cols <= 32 ? 2 : 1) * sms && steps >= 4 * split) split *= 2;
+  p.stages = Z::stages(p.cols, split);
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage + Z::sums(p.cols, split);
+  void* args[] = {&mb, &ma, &p};
+  return launch(fn, static_cast<unsigned>(tiles * split), sdq::mm4::kThreads, smem, c.stream, args, split);
 }
 
 }  // namespace
@@ -230,39 +260,10 @@ int sdq_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_
   if (st != SDQ_OK || m == 0 || n == 0) return st;
   int sms = 0;
   if (const int e = sdq_internal::sm_count(&sms)) return e;
-  if (m > 128) {
-    const Product c = {a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format, static_cast<cudaStream_t>(stream)};
-    return launch_pair(c, format & SDQ_FMT_E8M0 ? pair_of<Scales::kE8M0, 256>(format & SDQ_FMT_OUT_F32)
-                                                 : pair_of<Scales::kE4M3, 256>(format & SDQ_FMT_OUT_F32), sms);
-  }
-  // Up to 128 rows of a: they are the columns of the accumulator, as few as
-  // hold them, and the weights' rows are its lanes.
-  const bool swapped = m <= 128;
-  sdq::mm4::Params p = {};
-  p.sa = static_cast<const uint8_t*>(swapped ? b_s : a_s);
-  p.sb = static_cast<const uint8_t*>(swapped ? a_s : b_s);
-  p.ga = a_global;
-  p.gb = b_global;
-  p.out = static_cast<uint8_t*>(out);
-  p.ld_out = ld_out;
-  p.rows_a = swapped ? n : m;
-  p.rows_b = swapped ? m : n;
-  p.codes = static_cast<int32_t>(k);
-  p.tiles_k = static_cast<int32_t>(tiles_of(k, format));
-  p.swapped = swapped;
-  p.out_f32 = format & SDQ_FMT_OUT_F32 ? 1 : 0;
-  p.wait_limit_ns = sdq_internal::wait_limit();
-  const MatmulKernel kern = format & SDQ_FMT_E8M0 ? matmul_for<Scales::kE8M0>(p.rows_b) : matmul_for<Scales::kE4M3>(p.rows_b);
-  if (const int e = sdq_internal::device_status_word(&p.status)) return e;
-  CUtensorMap ma, mb;
-  if (const int e = sdq_internal::make_code_map(&ma, swapped ? b : a, k / 2, p.rows_a, swapped ? ld_b : ld_a, 128)) return e;
-  if (const int e = sdq_internal::make_code_map(&mb, swapped ? a : b, k / 2, p.rows_b, swapped ? ld_a : ld_b, kern.n)) return e;
-  const cudaError_t e = cudaFuncSetAttribute(kern.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kern.smem));
-  if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
-  p.grid_a = static_cast<int32_t>((p.rows_a + 127) / 128);
-  const int64_t grid = p.grid_a * ((p.rows_b + kern.n - 1) / kern.n);
-  void* args[] = {&ma, &mb, &p};
-  return launch(kern.fn, static_cast<unsigned>(grid), sdq::mm4::kThreads, kern.smem, static_cast<cudaStream_t>(stream), args);
+  const Product c = {a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format, static_cast<cudaStream_t>(stream)};
+  const bool e8m0 = format & SDQ_FMT_E8M0, f32 = format & SDQ_FMT_OUT_F32;
+  if (m <= 128) return e8m0 ? launch_strip<Scales::kE8M0>(c, sms) : launch_strip<Scales::kE4M3>(c, sms);
+  return launch_pair(c, e8m0 ? pair_of<Scales::kE8M0, 256>(f32) : pair_of<Scales::kE4M3, 256>(f32), sms);
 }
 
 }  // extern "C"

@@ -8,8 +8,8 @@
 // from tensor memory, where tcgen05.cp puts the 512-byte scale tiles as they
 // lie in memory (128 rows x 4 groups).
 //
-// One side of the product has 128 rows a CTA (the accumulator's lanes), the
-// other kN (its columns).
+// This file: what both forms of the kernel share, and the form for few rows of A
+// (matmul_strip_kernel).  The form for many is in fp4_matmul_pair.cuh.
 #pragma once
 
 #include <cuda.h>
@@ -31,42 +31,21 @@ constexpr int kMmas = kStepCodes / kMmaCodes;
 constexpr int kThreads = 192;               // a load warp, an mma warp, four epilogue warps
 
 struct Params {
-  const uint8_t* sa;       // scale tiles of the side with 128 rows a CTA
-  const uint8_t* sb;       // of the other side
+  const uint8_t* sb;       // scale tiles of B, whose rows are the accumulator's lanes
+  const uint8_t* sa;       // of A, whose rows are its columns
   const float* ga;         // scales per tensor, or null
   const float* gb;
-  uint8_t* out;
+  uint8_t* out;            // [rows_a, rows_b]
   int64_t ld_out;          // elements
-  int64_t rows_a, rows_b;  // rows of the two sides
+  int64_t rows_a, rows_b;
   int32_t codes;           // k
   int32_t tiles_k;         // scale tiles along k
-  int32_t grid_a;          // CTAs along the side with 128 rows each
-  int32_t swapped;         // out is [rows_b, rows_a] instead of [rows_a, rows_b]
+  int32_t cols;            // columns a CTA computes: a multiple of 16, at most 128
+  int32_t tiles_b;         // blocks of 128 rows of B
+  int32_t stages, stage;   // the shared-memory ring
   int32_t out_f32;         // fp32 elements instead of bf16
   int* status;
   uint64_t wait_limit_ns;
-};
-
-template <Scales S, int kN>
-struct Shape {
-  static constexpr int kScaleTiles = S == Scales::kE8M0 ? 2 : 4;   // scale tiles a stage holds per 128 rows
-  static constexpr int kBlocksB = kN > 128 ? 2 : 1;                // 128-row blocks of the other side
-  static constexpr int kCodesA = kRows * kStepBytes;
-  static constexpr int kCodesB = kN * kStepBytes;
-  static constexpr int kScaleA = kScaleTiles * 512;
-  static constexpr int kScaleB = kBlocksB * kScaleTiles * 512;
-  static constexpr int kStage = kCodesA + kCodesB + kScaleA + kScaleB;   // a multiple of 1024
-  static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
-  // tensor memory: the sums, then two sets of scales used in turn
-  static constexpr int kColsScaleA = kScaleTiles * 4;
-  static constexpr int kColsScaleB = kScaleTiles * 4 * kBlocksB;
-  static constexpr int kColsScale = kColsScaleA + kColsScaleB;
-  static constexpr int kColsSum = kN < 32 ? 32 : kN;
-  static constexpr int kColsUsed = kColsSum + 2 * kColsScale;
-  static constexpr int kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStage);
-  static_assert(kColsUsed <= 512, "tensor memory has 512 columns");
-  static_assert(kStage % 1024 == 0, "the swizzled boxes start on 1024 bytes");
 };
 
 // True in one lane of a converged warp.  A branch on it, unlike one on the lane's
@@ -132,6 +111,15 @@ __device__ __forceinline__ void load_sums32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void load_sums16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Shared-memory descriptors (start address, strides in units of 16 bytes,
@@ -148,10 +136,10 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
 // (format 1 at bits 7 and 10), n / 8 at bit 17, E8M0 scales at bit 23,
 // m / 128 at bit 27; the scale's first byte in its column word goes to bits 4
 // (B) and 29 (A).
-template <Scales S, int kN>
-__device__ __forceinline__ uint32_t instruction(uint32_t scale_byte) {
-  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kN / 8) << 17) | (S == Scales::kE8M0 ? 1u << 23 : 0u) |
-         (1u << 27) | (scale_byte << 4) | (scale_byte << 29);
+template <Scales S>
+__device__ __forceinline__ uint32_t instruction(int m, int n, uint32_t scale_byte) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n / 8) << 17) | (S == Scales::kE8M0 ? 1u << 23 : 0u) |
+         (static_cast<uint32_t>(m / 128) << 27) | (scale_byte << 4) | (scale_byte << 29);
 }
 
 // Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
@@ -196,7 +184,49 @@ __device__ __forceinline__ bool wait(const Sync& y, uint32_t bar, uint32_t parit
   return true;
 }
 
-// ---- the kernel -----------------------------------------------------------------
+// ---- clusters -----------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address, for the whole cluster, of this shared-memory address in CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float load_shared(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// ---- the kernel for few rows of A -----------------------------------------------------
+//
+// Reading B bounds it.  B's rows are the accumulator's lanes, 128 a CTA, and A's its
+// columns, so an instruction is no wider than A needs.  The CTAs of a cluster take
+// the steps along k in turn, so that there are about as many CTAs as the device
+// holds; each sends its sums to the CTA that a column belongs to (column c to rank
+// c mod the cluster's size), which adds them up in the order of the ranks: the
+// result does not depend on timing.  (Sending takes one barrier of the cluster;
+// reading the others' sums took two, and a latency a number.)  Up to 32 columns
+// two CTAs fit a multiprocessor: a kernel's set-up is under way while the one
+// before it still runs.
 
 __device__ __forceinline__ void store_out(const Params& p, int64_t row, int64_t col, float v) {
   const int64_t at = row * p.ld_out + col;
@@ -206,84 +236,107 @@ __device__ __forceinline__ void store_out(const Params& p, int64_t row, int64_t 
     reinterpret_cast<uint16_t*>(p.out)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
 }
 
-template <Scales S, int kN>
-__global__ void __launch_bounds__(kThreads, 1)
-    matmul_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const Params p) {
-  using Z = Shape<S, kN>;
+constexpr int kMaxStages = 8;
+
+template <Scales S>
+struct StripShape {
+  static constexpr int kScaleTiles = S == Scales::kE8M0 ? 2 : 4;   // scale tiles a stage holds of either side
+  static constexpr int kScale = kScaleTiles * 512;
+  static constexpr int kCodesB = kRows * kStepBytes;
+  static constexpr int kColsScale = 2 * kScaleTiles * 4;           // tensor memory: a set of both sides' scales
+  static constexpr int kCols = 256;                                // 128 sums and two sets of scales used in turn
+  static_assert(128 + 2 * kColsScale <= kCols, "the sums and the scales fit");
+  static int stage(int cols) { return kCodesB + cols * kStepBytes + 2 * kScale; }   // a multiple of 1024
+  static int sums(int cols, int split) { return split > 1 ? (cols + split - 1) / split * split * kRows * 4 : 0; }
+  static int stages(int cols, int split) {
+    const int n = ((cols <= 32 ? 108 : 208) * 1024 - sums(cols, split)) / stage(cols);
+    return n > kMaxStages ? kMaxStages : n;
+  }
+};
+
+template <Scales S>
+__global__ void __launch_bounds__(kThreads, 2)
+    matmul_strip_kernel(const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap ma, const Params p) {
+  using Z = StripShape<S>;
   extern __shared__ uint8_t raw[];
-  __shared__ alignas(8) uint64_t bars[2 * Z::kStages + 1];
+  __shared__ alignas(8) uint64_t bars[2 * kMaxStages + 1];
   __shared__ uint32_t tmem_addr;
   __shared__ int abort_flag, issued_flag;
-  const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * Z::kStages, done = empty + 8 * Z::kStages;
+  const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;   // the same offset in every CTA of the cluster
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages, done = empty + 8 * kMaxStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+  const int tile = blockIdx.x / ranks;
+  const int tile_a = tile / p.tiles_b, tile_b = tile - tile_a * p.tiles_b;
+  const int64_t b0 = static_cast<int64_t>(tile_b) * kRows, a0 = static_cast<int64_t>(tile_a) * p.cols;
+  const int steps_all = (p.codes + kStepCodes - 1) / kStepCodes;
+  const int steps = (steps_all - rank + ranks - 1) / ranks;   // steps rank, rank + ranks, ...: at least one
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * Z::kStages + 1; ++i) mbar_init(full + 8 * i, 1);
+    prefetch_tensormap(&mb);
+    prefetch_tensormap(&ma);
+    for (int i = 0; i < 2 * kMaxStages + 1; ++i) mbar_init(full + 8 * i, 1);
     fence_mbar_init();
     abort_flag = 0;
     issued_flag = 0;
   }
+  if (warp == 0 && elect_one())   // into L2 only: changes no value that is read after the wait below
+    for (int i = 0; i < steps && i < p.stages; ++i)
+      tma_prefetch_l2_2d(&mb, (rank + i * ranks) * kStepBytes, static_cast<int32_t>(b0));
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_addr), Z::kCols);
     tmem_relinquish();
     fence_before();
   }
   __syncthreads();
+  if (ranks > 1) cluster_arrive();   // waited for before the first store into another CTA: all have started
   fence_after();
   grid_dependency_wait();     // operands may come from the previous kernel in the stream
   grid_launch_dependents();   // after the allocation: a later kernel's cannot come first
   const uint32_t tmem = *const_cast<volatile uint32_t*>(&tmem_addr);
   const Sync sync = {p.status, &abort_flag, p.wait_limit_ns};
-  const int steps = (p.codes + kStepCodes - 1) / kStepCodes;
-  const int tile_b = blockIdx.x / p.grid_a, tile_a = blockIdx.x - tile_b * p.grid_a;
-  const int64_t a0 = static_cast<int64_t>(tile_a) * kRows, b0 = static_cast<int64_t>(tile_b) * kN;
-  const int blocks_b = static_cast<int>(min(static_cast<int64_t>(Z::kBlocksB), (p.rows_b - b0 + 127) / 128));
+  const uint32_t parts = ring + p.stages * p.stage;   // the sums that this CTA receives
+  const int share = (p.cols + ranks - 1) / ranks;     // columns that belong to a CTA
 
   if (warp == 0) {
     if (elect_one()) {
       for (int i = 0; i < steps; ++i) {
-        const int st = i % Z::kStages;
-        if (i >= Z::kStages && !wait(sync, empty + 8 * st, ((i / Z::kStages) - 1) & 1)) break;
-        const uint32_t buf = ring + st * Z::kStage, bar = full + 8 * st;
-        const int k_tile = i * Z::kScaleTiles;
+        const int st = i % p.stages, step = rank + i * ranks;
+        if (i >= p.stages && !wait(sync, empty + 8 * st, ((i / p.stages) - 1) & 1)) break;
+        const uint32_t buf = ring + st * p.stage, bar = full + 8 * st;
+        const int k_tile = step * Z::kScaleTiles;
         const int tiles = min(Z::kScaleTiles, p.tiles_k - k_tile);
-        mbar_arrive_expect_tx(bar, Z::kCodesA + Z::kCodesB + (1 + blocks_b) * tiles * 512);
-        tma_load(buf, &ma, bar, i * kStepBytes, static_cast<int32_t>(a0));
-        tma_load(buf + Z::kCodesA, &mb, bar, i * kStepBytes, static_cast<int32_t>(b0));
-        const uint32_t sc = buf + Z::kCodesA + Z::kCodesB;
-        bulk_load(sc, p.sa + ((a0 >> 7) * p.tiles_k + k_tile) * 512, tiles * 512, bar);
-        for (int b = 0; b < blocks_b; ++b)
-          bulk_load(sc + Z::kScaleA + b * Z::kScaleTiles * 512, p.sb + (((b0 >> 7) + b) * p.tiles_k + k_tile) * 512,
-                    tiles * 512, bar);
+        mbar_arrive_expect_tx(bar, Z::kCodesB + p.cols * kStepBytes + 2 * tiles * 512);
+        tma_load(buf, &mb, bar, step * kStepBytes, static_cast<int32_t>(b0));
+        tma_load(buf + Z::kCodesB, &ma, bar, step * kStepBytes, static_cast<int32_t>(a0));
+        const uint32_t sc = buf + Z::kCodesB + p.cols * kStepBytes;
+        bulk_load(sc, p.sb + (static_cast<int64_t>(tile_b) * p.tiles_k + k_tile) * 512, tiles * 512, bar);
+        bulk_load(sc + Z::kScale, p.sa + ((a0 >> 7) * p.tiles_k + k_tile) * 512, tiles * 512, bar);
         issued_flag = i + 1;
       }
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      bool ok = true;
-      for (int i = 0; i < steps && ok; ++i) {
-        const int st = i % Z::kStages;
-        ok = wait(sync, full + 8 * st, (i / Z::kStages) & 1);
-        if (!ok) break;
+      const uint32_t id0 = instruction<S>(kRows, p.cols, 0), id1 = S == Scales::kE8M0 ? instruction<S>(kRows, p.cols, 2) : id0;
+      for (int i = 0; i < steps; ++i) {
+        const int st = i % p.stages, step = rank + i * ranks;
+        if (!wait(sync, full + 8 * st, (i / p.stages) & 1)) break;
         fence_after();
-        const uint32_t buf = ring + st * Z::kStage;
-        const uint32_t ta = tmem + Z::kColsSum + (i & 1) * Z::kColsScale, tb = ta + Z::kColsScaleA;
-        const uint64_t ds = desc_scales(buf + Z::kCodesA + Z::kCodesB);
+        const uint32_t buf = ring + st * p.stage;
+        const uint32_t tb = tmem + 128 + (i & 1) * Z::kColsScale, ta = tb + Z::kScaleTiles * 4;
+        const uint64_t ds = desc_scales(buf + Z::kCodesB + p.cols * kStepBytes);
 #pragma unroll
         for (int j = 0; j < Z::kScaleTiles; ++j) {
-          copy_scales(ta + 4 * j, ds + 32 * j);
-#pragma unroll
-          for (int b = 0; b < Z::kBlocksB; ++b)
-            copy_scales(tb + 4 * (j * Z::kBlocksB + b), ds + (Z::kScaleA >> 4) + 32 * (b * Z::kScaleTiles + j));
+          copy_scales(tb + 4 * j, ds + 32 * j);
+          copy_scales(ta + 4 * j, ds + (Z::kScale >> 4) + 32 * j);
         }
-        const uint64_t da = desc_codes(buf), db = desc_codes(buf + Z::kCodesA);
-        const int mmas = min(kMmas, (p.codes - i * kStepCodes + kMmaCodes - 1) / kMmaCodes);
+        const uint64_t db = desc_codes(buf), da = desc_codes(buf + Z::kCodesB);
+        const int mmas = min(kMmas, (p.codes - step * kStepCodes + kMmaCodes - 1) / kMmaCodes);
 #pragma unroll
         for (int j = 0; j < kMmas; ++j) {
           constexpr int kPerTile = S == Scales::kE8M0 ? 2 : 1;   // products a scale tile lasts
           if (j < mmas)
-            mma<S>(tmem, da + 2 * j, db + 2 * j, instruction<S, kN>(S == Scales::kE8M0 ? 2 * (j & 1) : 0),
-                   ta + 4 * (j / kPerTile), tb + 4 * (j / kPerTile) * Z::kBlocksB, i > 0 || j > 0);
+            mma<S>(tmem, db + 2 * j, da + 2 * j, (j & 1) ? id1 : id0, tb + 4 * (j / kPerTile), ta + 4 * (j / kPerTile),
+                   i > 0 || j > 0);
         }
         commit(empty + 8 * st);
       }
@@ -291,39 +344,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(done, 0, sync.limit_ns);   // nothing of the tensor cores is in flight when the CTA frees its memory
     }
   } else {
-    const bool ok = wait(sync, done, 0);
+    const bool ok = wait(sync, done, 0) && !*sync.abort;
     fence_after();
-    if (ok && !*sync.abort) {
-      const int quarter = warp & 3;   // the lanes a warp may read
-      const int64_t ra = a0 + quarter * 32 + lane;
-      const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f);
-#pragma unroll 1
-      for (int c = 0; c < kN; c += 32) {
-        if (b0 + c >= p.rows_b) break;
-        uint32_t r[32];
-        load_sums32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, r);
-        load_wait();
-        if (ra < p.rows_a) {
+    const int quarter = warp & 3;   // the lanes a warp may read
+    const int row = quarter * 32 + lane;
+    const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f);
+    const int cols = static_cast<int>(min(static_cast<int64_t>(p.cols), p.rows_a - a0));
+    if (ranks > 1) {
+      __syncwarp();
+      cluster_wait();
+    }
+    for (int c = 0; ok && c < cols; c += 16) {
+      uint32_t r[16];
+      load_sums16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, r);
+      load_wait();
+      if (ranks > 1) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int64_t rb = b0 + c + e;
-            if (c + e < kN && rb < p.rows_b) {
-              const float v = __uint_as_float(r[e]) * alpha;
-              if (p.swapped)
-                store_out(p, rb, ra, v);
-              else
-                store_out(p, ra, rb, v);
-            }
-          }
+        for (int e = 0; e < 16; ++e) {
+          const int owner = (c + e) % ranks, j = (c + e) / ranks;
+          store_cluster(at_rank(parts + ((rank * share + j) * kRows + row) * 4, owner), r[e]);
         }
+      } else if (b0 + row < p.rows_b) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (c + e < cols) store_out(p, a0 + c + e, b0 + row, __uint_as_float(r[e]) * alpha);
       }
     }
     fence_before();
+    if (ranks > 1) {   // (after a wait that ran out the sums are of no use, as the status says)
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      if (b0 + row < p.rows_b) {
+        for (int j = 0; j * ranks + rank < cols; ++j) {
+          float v = load_shared(parts + (j * kRows + row) * 4);
+#pragma unroll
+          for (int r = 1; r < 8; ++r)
+            if (r < ranks) v += load_shared(parts + ((r * share + j) * kRows + row) * 4);
+          store_out(p, a0 + j * ranks + rank, b0 + row, v * alpha);
+        }
+      }
+    }
+  }
+  if (warp < 2 && ranks > 1) {   // the barriers count every thread
+    __syncwarp();
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
   }
   __syncthreads();
   if (threadIdx.x == 0 && abort_flag) {   // copies still in flight write this CTA's shared memory
-    for (int i = max(0, issued_flag - Z::kStages); i < issued_flag; ++i)
-      mbar_wait(full + 8 * (i % Z::kStages), (i / Z::kStages) & 1, sync.limit_ns);
+    for (int i = max(0, issued_flag - p.stages); i < issued_flag; ++i)
+      mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1, sync.limit_ns);
   }
   __syncthreads();
   __syncwarp();

@@ -59,20 +59,6 @@ struct PairParams {
 
 // ---- pairs ------------------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address, for the whole cluster, of this shared-memory address in CTA `rank`.
-__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -106,13 +92,6 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
         "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
-}
-
-// As instruction(), for 256 rows.
-template <Scales S, int kN>
-__device__ __forceinline__ uint32_t instruction_pair(uint32_t scale_byte) {
-  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kN / 8) << 17) | (S == Scales::kE8M0 ? 1u << 23 : 0u) |
-         (2u << 27) | (scale_byte << 4) | (scale_byte << 29);
 }
 
 // ---- the epilogue's stores ----------------------------------------------------------
@@ -297,7 +276,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           for (int j = 0; j < kMmas; ++j) {
             constexpr int kPerTile = S == Scales::kE8M0 ? 2 : 1;   // products a scale tile lasts
             if (j < mmas)
-              mma_pair<S>(acc, da + 2 * j, db + 2 * j, instruction_pair<S, kN>(S == Scales::kE8M0 ? 2 * (j & 1) : 0),
+              mma_pair<S>(acc, da + 2 * j, db + 2 * j, instruction<S>(256, kN, S == Scales::kE8M0 ? 2 * (j & 1) : 0),
                           ca + 4 * (j / kPerTile), cb + 4 * (j / kPerTile) * Z::kBlocksB, i > 0 || j > 0);
           }
           commit_pair(empty + 8 * st);
