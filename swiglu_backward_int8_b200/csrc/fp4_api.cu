@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include "fp4_kernel.cuh"
 #include "fp4_matmul.cuh"
@@ -48,6 +49,22 @@ int launch(const void* kernel, unsigned grid, unsigned block, size_t smem, cudaS
   return e == cudaSuccess ? SDQ_OK : sdq_internal::cuda_fail(e);
 }
 
+// Sets a kernel's shared-memory limit once a device.
+struct SmemLimit {
+  std::once_flag once[64];
+  cudaError_t err[64] = {};
+  int set(const void* kernel, int bytes) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
+    if (dev < 0 || dev >= 64) return sdq_internal::cuda_fail(cudaErrorInvalidDevice);
+    std::call_once(once[dev], [&] {
+      err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    return err[dev] == cudaSuccess ? SDQ_OK : sdq_internal::cuda_fail(err[dev]);
+  }
+};
+
 template <Scales S>
 const void* quantize_kernel(bool rows, bool cols) {
   if (rows && cols) return reinterpret_cast<const void*>(sdq::fp4::quantize_kernel<S, true, true>);
@@ -59,13 +76,15 @@ struct MatmulKernel {
   const void* fn;
   size_t smem;
   int n;
+  SmemLimit* limit;
 };
 
 template <Scales S, int kN>
 MatmulKernel pair_of(bool f32) {
+  static SmemLimit limits[2];
   return {f32 ? reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kN, true>)
               : reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kN, false>),
-          sdq::mm4::PairShape<S, kN>::kSmem, kN};
+          sdq::mm4::PairShape<S, kN>::kSmem, kN, &limits[f32]};
 }
 
 // One call of the product, checked.
@@ -103,8 +122,7 @@ int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
   if (const int e = sdq_internal::make_scale_map(&msb, c.b_s, tiles_k, (c.n + 127) / 128, stage)) return e;
   if (p.vec)
     if (const int e = sdq_internal::make_out_map(&mo, c.out, f32, c.n, c.m, c.ld_out)) return e;
-  const cudaError_t e = cudaFuncSetAttribute(kern.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kern.smem));
-  if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
+  if (const int e = kern.limit->set(kern.fn, static_cast<int>(kern.smem))) return e;
   const int64_t pairs = std::min<int64_t>(sms / 2, int64_t{p.tiles_a} * p.tiles_b);
   void* args[] = {&ma, &mb, &msa, &msb, &mo, &p};
   return launch(kern.fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kPairThreads, kern.smem, c.stream, args);
@@ -135,8 +153,8 @@ int launch_strip(const Product& c, int sms) {
   if (const int e = sdq_internal::make_code_map(&mb, c.b, c.k / 2, c.n, c.ld_b, 128)) return e;
   if (const int e = sdq_internal::make_code_map(&ma, c.a, c.k / 2, c.m, c.ld_a, p.cols)) return e;
   const void* fn = reinterpret_cast<const void*>(sdq::mm4::matmul_strip_kernel<S>);
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 210 * 1024);
-  if (e != cudaSuccess) return sdq_internal::cuda_fail(e);
+  static SmemLimit limit;
+  if (const int e = limit.set(fn, 210 * 1024)) return e;
   const int64_t tiles = p.tiles_b * ((c.m + p.cols - 1) / p.cols);
   const int64_t steps = (c.k + sdq::mm4::kStepCodes - 1) / sdq::mm4::kStepCodes;
   int split = 1;

@@ -26,6 +26,8 @@ from ._lib import (FMT_E2M1, FMT_E4M3, FMT_E8M0, FMT_OUT_F32, FMT_SCALE_E4M3, FM
 
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
+_U8 = (torch.uint8,)
+_WEIGHT = (torch.bfloat16, torch.float32)
 _CODES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn, "e2m1": torch.uint8}
 _CODES_OF = {torch.int8: "int8", torch.float8_e4m3fn: "e4m3", torch.uint8: "e2m1"}
 _SCALES = {"fp32": torch.float32, "e8m0": torch.float8_e8m0fnu, "e4m3": torch.float8_e4m3fn}
@@ -58,15 +60,33 @@ def _scales_of(s: Optional[torch.Tensor], given: Optional[str], default: str) ->
 
 def _tiles(name: str, s: torch.Tensor, rows: int, k: int, scales: str, device) -> int:
     """Check scale tiles; returns their address."""
-    shape = fp4_scale_shape(rows, k, scales)
-    if s.shape != shape or _SCALES_OF.get(s.dtype) != scales or not s.is_contiguous() or s.device != device:
+    shape = (-(-rows // 128), -(-(k // _FP4_GROUP[scales]) // 4), 512)
+    if s.shape != shape or _SCALES_OF.get(s.dtype) != scales or s.get_device() != device.index or not s.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {scales} scale tiles {shape} on {device}, got {s.dtype} "
                          f"{tuple(s.shape)} on {s.device}")
     return s.data_ptr()
 
 
+def _ld(name: str, t: torch.Tensor, rows: int, cols: int, dtypes, device) -> int:
+    """The leading dimension of a 2-D row-major operand.  A small call spends
+    most of its time in such checks: what is in order passes here, the rest goes
+    to the check that says what is wrong."""
+    if t.dtype in dtypes and t.shape == (rows, cols) and t.get_device() == device.index:
+        ld, unit = t.stride()
+        if unit == 1 and ld >= cols and rows > 1:
+            return ld
+        if unit == 1 and rows == 1:
+            return cols
+    return _rows(name, t, (rows, cols), dtypes, True, device)
+
+
 def _codes(name: str, q: torch.Tensor, rows: int, k: int, device) -> int:
-    return _rows(name, q, (rows, k // 2), (torch.uint8,), True, device)
+    return _ld(name, q, rows, k // 2, _U8, device)
+
+
+def _length(k: int) -> None:
+    if k < 32 or k % 32:
+        raise ValueError(f"k={k} must be a positive multiple of 32")
 
 
 def _one(name: str, g: Optional[torch.Tensor], scales: str, device) -> Optional[int]:
@@ -75,13 +95,13 @@ def _one(name: str, g: Optional[torch.Tensor], scales: str, device) -> Optional[
         return None
     if scales != "e4m3":
         raise ValueError(f"{name} goes with \"e4m3\" scales")
-    if g.numel() != 1 or g.dtype != torch.float32 or g.device != device:
+    if g.numel() != 1 or g.dtype != torch.float32 or g.get_device() != device.index:
         raise ValueError(f"{name} must be one float32 on {device}")
     return g.data_ptr()
 
 
 def _vector(name: str, v: torch.Tensor, n: int, dtypes, device) -> int:
-    if tuple(v.shape) != (n,) or v.dtype not in dtypes or not v.is_contiguous() or v.device != device:
+    if v.shape != (n,) or v.dtype not in dtypes or v.get_device() != device.index or not v.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {' or '.join(map(str, dtypes))} [{n}] on {device}, got {v.dtype} "
                          f"{tuple(v.shape)} on {v.device}")
     return v.data_ptr()
@@ -97,11 +117,20 @@ def _two_d(name: str, t: torch.Tensor) -> Tuple[int, int]:
 
 def _call(entry, device, *args) -> None:
     """The entry point on the device's current stream."""
-    if torch.cuda.current_device() == device.index:
-        entry(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        entry(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            entry(*args, torch.cuda.current_stream(device).cuda_stream)
+            entry(*args, _raw_stream(index))
+
+
+def _stream_of(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# (the stream's address without a Stream object around it, 2 us cheaper)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 
 
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -143,14 +172,14 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
     fmt = {"int8": 0, "e4m3": FMT_E4M3, "e2m1": FMT_E2M1}[codes] | \
         {"fp32": 0, "e8m0": FMT_E8M0, "e4m3": FMT_SCALE_E4M3}[scales] | \
         (FMT_WEIGHT_F32 if weight.dtype == torch.float32 else 0)
-    ld_x = _rows("x", x, (rows, channels), _BF16, True, dev)
-    wp = _vector("weight", weight, channels, (torch.bfloat16, torch.float32), dev)
+    ld_x = _ld("x", x, rows, channels, _BF16, dev)
+    wp = _vector("weight", weight, channels, _WEIGHT, dev)
     rp, ld_r, hp, ld_h = None, 0, None, 0
     if residual is not None:
-        rp, ld_r = residual.data_ptr(), _rows("residual", residual, (rows, channels), _BF16, True, dev)
+        rp, ld_r = residual.data_ptr(), _ld("residual", residual, rows, channels, _BF16, dev)
         if h is None:
             h = torch.empty((rows, channels), dtype=torch.bfloat16, device=dev)
-        hp, ld_h = h.data_ptr(), _rows("h", h, (rows, channels), _BF16, True, dev)
+        hp, ld_h = h.data_ptr(), _ld("h", h, rows, channels, _BF16, dev)
     elif h is not None:
         raise ValueError("h is written only with a residual")
     else:
@@ -168,11 +197,11 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
             q = torch.empty((rows, channels), dtype=_CODES[codes], device=dev)
         if s is None:
             s = torch.empty((rows, groups), dtype=_SCALES[scales], device=dev)
-        ld_q = _rows("q", q, (rows, channels), (_CODES[codes],), True, dev)
-        ld_s = _rows("s", s, (rows, groups), (s.dtype,), True, dev)
+        ld_q = _ld("q", q, rows, channels, (_CODES[codes],), dev)
+        ld_s = _ld("s", s, rows, groups, (s.dtype,), dev)
     yp, ld_y = None, 0
     if y is not None:
-        yp, ld_y = y.data_ptr(), _rows("y", y, (rows, channels), _BF16, True, dev)
+        yp, ld_y = y.data_ptr(), _ld("y", y, rows, channels, _BF16, dev)
     _call(sdq_rmsnorm_quant, dev, x.data_ptr(), ld_x, rp, ld_r, wp, hp, ld_h, q.data_ptr(), ld_q, s.data_ptr(), ld_s,
           yp, ld_y, None if rstd is None else _vector("rstd", rstd, rows, _F32, dev),
           _one("global_scale", global_scale, scales, dev), rows, channels, group_size, fmt, eps)
@@ -195,13 +224,13 @@ def rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     need = sdq_rmsnorm_backward_workspace_bytes(rows, channels)
     if need == 0:
         raise ValueError(f"{channels} channels: a positive multiple of 16 is needed")
-    ld_gy = _rows("grad_y", grad_y, (rows, channels), _BF16, True, dev)
-    ld_h = _rows("h", h, (rows, channels), _BF16, True, dev)
-    wp = _vector("weight", weight, channels, (torch.bfloat16, torch.float32), dev)
+    ld_gy = _ld("grad_y", grad_y, rows, channels, _BF16, dev)
+    ld_h = _ld("h", h, rows, channels, _BF16, dev)
+    wp = _vector("weight", weight, channels, _WEIGHT, dev)
     sp = _vector("rstd", rstd, rows, _F32, dev)
     ghp, ld_gh = None, 0
     if grad_h is not None:
-        ghp, ld_gh = grad_h.data_ptr(), _rows("grad_h", grad_h, (rows, channels), _BF16, True, dev)
+        ghp, ld_gh = grad_h.data_ptr(), _ld("grad_h", grad_h, rows, channels, _BF16, dev)
     if grad_x is None:
         grad_x = torch.empty((rows, channels), dtype=torch.bfloat16, device=dev)
     if grad_weight is None:
@@ -211,7 +240,7 @@ def rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
     _call(sdq_rmsnorm_backward, dev, grad_y.data_ptr(), ld_gy, h.data_ptr(), ld_h, wp, sp, ghp, ld_gh,
-          grad_x.data_ptr(), _rows("grad_x", grad_x, (rows, channels), _BF16, True, dev),
+          grad_x.data_ptr(), _ld("grad_x", grad_x, rows, channels, _BF16, dev),
           _vector("grad_weight", grad_weight, channels, _F32, dev), rows, channels,
           FMT_WEIGHT_F32 if weight.dtype == torch.float32 else 0, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
@@ -235,7 +264,7 @@ def quantize_fp4(x: torch.Tensor, scales: Optional[str] = None, axis: str = "row
         raise ValueError(f"axis is \"rows\", \"columns\" or \"both\", not {axis!r}")
     scales = _scales_of(s if s is not None else s_t, scales, "e8m0")
     fp4_scale_shape(rows, channels, scales)   # channels a multiple of 32, 4-bit scales
-    ld_x = _rows("x", x, (rows, channels), _BF16, True, dev)
+    ld_x = _ld("x", x, rows, channels, _BF16, dev)
     padded = -(-rows // 32) * 32
     out: list = []
     args: list = []
@@ -268,11 +297,12 @@ def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, global_scale: Optional[torc
     k *= 2
     dev = q.device
     scales = _scales_of(s, None, "e8m0")
+    _length(k)
     ld_q, sp = _codes("q", q, rows, k, dev), _tiles("s", s, rows, k, scales, dev)
     if out is None:
         out = torch.empty((rows, k), dtype=torch.bfloat16, device=dev)
     _call(sdq_dequantize_fp4, dev, q.data_ptr(), ld_q, sp, _one("global_scale", global_scale, scales, dev),
-          out.data_ptr(), _rows("out", out, (rows, k), _BF16, True, dev), rows, k, _FP4_FORMAT[scales])
+          out.data_ptr(), _ld("out", out, rows, k, _BF16, dev), rows, k, _FP4_FORMAT[scales])
     return out
 
 
@@ -288,13 +318,14 @@ def matmul_fp4(a: torch.Tensor, a_s: torch.Tensor, b: torch.Tensor, b_s: torch.T
         raise ValueError(f"a has rows of {2 * ka} codes and b of {2 * kb}")
     k, dev = 2 * ka, a.device
     scales = _scales_of(a_s, None, "e8m0")
+    _length(k)
     ld_a, ld_b = _codes("a", a, m, k, dev), _codes("b", b, n, k, dev)
     ap, bp = _tiles("a_s", a_s, m, k, scales, dev), _tiles("b_s", b_s, n, k, scales, dev)
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")
-    ld_out = _rows("out", out, (m, n), (torch.bfloat16, torch.float32), True, dev)
+    ld_out = _ld("out", out, m, n, _WEIGHT, dev)
     _call(sdq_matmul_fp4, dev, a.data_ptr(), ld_a, ap, _one("a_global", a_global, scales, dev), b.data_ptr(), ld_b, bp,
           _one("b_global", b_global, scales, dev), out.data_ptr(), ld_out, m, n, k,
           _FP4_FORMAT[scales] | (FMT_OUT_F32 if out.dtype == torch.float32 else 0))
