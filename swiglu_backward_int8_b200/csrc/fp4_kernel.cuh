@@ -63,11 +63,9 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
     if (act) v = *reinterpret_cast<const uint4*>(p.x + 2 * ((m0 + r) * p.ld_x + k0 + c8));
     if (kCols) *reinterpret_cast<uint4*>(tile + r * kPitch + c8 * 2) = v;
     if (kRows) {
-      float y[8];
+      float2 y[4];
       quant::unpack8(v, y);
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, quant::mag(y[e]));
+      uint32_t m = quant::amax8(y);
 #pragma unroll
       for (int d = 1; d < G / 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
       const quant::GroupScale gs = quant::group_scale<Codes::kE2M1, S>(m, g);
@@ -94,25 +92,27 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
     for (int i = 0; i < kGroups / 4; ++i) {
       const int grp = (t >> 6) + 4 * i;         // the group of rows
       uint32_t v[G];
-      uint32_t ma = 0, mb = 0;
+      float ma = 0.0f, mb = 0.0f;
 #pragma unroll
-      for (int e = 0; e < G; ++e) {
-        v[e] = *reinterpret_cast<const uint32_t*>(tile + (grp * G + e) * kPitch + c * 2);
-        ma = max(ma, quant::mag(bf16_lo(v[e])));
-        mb = max(mb, quant::mag(bf16_hi(v[e])));
+      for (int e = 0; e < G; ++e) v[e] = *reinterpret_cast<const uint32_t*>(tile + (grp * G + e) * kPitch + c * 2);
+#pragma unroll
+      for (int e = 0; e < G; e += 2) {
+        ma = quant::amax3(ma, bf16_lo(v[e]), bf16_lo(v[e + 1]));
+        mb = quant::amax3(mb, bf16_hi(v[e]), bf16_hi(v[e + 1]));
       }
-      const quant::GroupScale ga = quant::group_scale<Codes::kE2M1, S>(ma, g), gb = quant::group_scale<Codes::kE2M1, S>(mb, g);
+      const quant::GroupScale ga = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(ma), g);
+      const quant::GroupScale gb = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(mb), g);
       const int64_t row = m0 + grp * G;
       const bool in = row < p.rows_padded;      // whole groups: rows_padded is a multiple of 32
       uint32_t qa[G / 8], qb[G / 8];
 #pragma unroll
       for (int w = 0; w < G / 8; ++w) {
-        float y[8];
+        float2 y[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = bf16_lo(v[w * 8 + e]);
+        for (int e = 0; e < 4; ++e) y[e] = make_float2(bf16_lo(v[w * 8 + 2 * e]), bf16_lo(v[w * 8 + 2 * e + 1]));
         qa[w] = quant::codes8<Codes::kE2M1, S>(y, ga).x;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = bf16_hi(v[w * 8 + e]);
+        for (int e = 0; e < 4; ++e) y[e] = make_float2(bf16_hi(v[w * 8 + 2 * e]), bf16_hi(v[w * 8 + 2 * e + 1]));
         qb[w] = quant::codes8<Codes::kE2M1, S>(y, gb).x;
       }
       if (in && c < nch) {

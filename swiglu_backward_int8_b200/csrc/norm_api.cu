@@ -16,22 +16,28 @@ using sdq::norm::Params;
 using sdq::quant::Codes;
 using sdq::quant::Scales;
 
-using Kernel = void (*)(Params, int);
+// The kernel for a format: one or two vectors a thread for a row, four with the
+// next row loaded ahead, or (vecs 0) the one for long rows.
+template <Codes C, Scales S>
+const void* kernel_of(int vecs, bool ahead) {
+  using sdq::norm::rmsnorm_quant_kernel;
+  if (vecs == 0) return reinterpret_cast<const void*>(sdq::norm::rmsnorm_quant_long_kernel<C, S>);
+  if (ahead) return reinterpret_cast<const void*>(sdq::norm::rmsnorm_quant_rows_kernel<C, S>);
+  return vecs == 1 ? reinterpret_cast<const void*>(rmsnorm_quant_kernel<C, S, 1>)
+                   : reinterpret_cast<const void*>(rmsnorm_quant_kernel<C, S, 2>);
+}
+
+const void* kernel_for(uint32_t format, int vecs, bool ahead) {
+  const bool e8 = format & SDQ_FMT_E8M0;
+  if (format & SDQ_FMT_E2M1)
+    return e8 ? kernel_of<Codes::kE2M1, Scales::kE8M0>(vecs, ahead) : kernel_of<Codes::kE2M1, Scales::kE4M3>(vecs, ahead);
+  if (format & SDQ_FMT_E4M3)
+    return e8 ? kernel_of<Codes::kE4M3, Scales::kE8M0>(vecs, ahead) : kernel_of<Codes::kE4M3, Scales::kF32>(vecs, ahead);
+  return e8 ? kernel_of<Codes::kInt8, Scales::kE8M0>(vecs, ahead) : kernel_of<Codes::kInt8, Scales::kF32>(vecs, ahead);
+}
 
 constexpr uint32_t kFormatBits = SDQ_FMT_E4M3 | SDQ_FMT_E8M0 | SDQ_FMT_E2M1 | SDQ_FMT_SCALE_E4M3 | SDQ_FMT_WEIGHT_F32;
 constexpr int64_t kMaxParts = 592;   // rows of partial weight gradients a backward keeps: four a multiprocessor
-
-template <int V>
-Kernel kernel_of(uint32_t format) {
-  if (format & SDQ_FMT_E2M1)
-    return format & SDQ_FMT_E8M0 ? sdq::norm::rmsnorm_quant_kernel<Codes::kE2M1, Scales::kE8M0, V>
-                                 : sdq::norm::rmsnorm_quant_kernel<Codes::kE2M1, Scales::kE4M3, V>;
-  if (format & SDQ_FMT_E4M3)
-    return format & SDQ_FMT_E8M0 ? sdq::norm::rmsnorm_quant_kernel<Codes::kE4M3, Scales::kE8M0, V>
-                                 : sdq::norm::rmsnorm_quant_kernel<Codes::kE4M3, Scales::kF32, V>;
-  return format & SDQ_FMT_E8M0 ? sdq::norm::rmsnorm_quant_kernel<Codes::kInt8, Scales::kE8M0, V>
-                               : sdq::norm::rmsnorm_quant_kernel<Codes::kInt8, Scales::kF32, V>;
-}
 
 // The codes' and scales' formats go together: 8-bit codes with fp32 or E8M0
 // scales, E2M1 codes with E8M0 or E4M3 scales.
@@ -70,6 +76,13 @@ int launch(const void* kernel, dim3 grid, dim3 block, cudaStream_t stream, void*
 }
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
+
+// CTAs of `threads` threads with `regs` registers each that a multiprocessor
+// holds: each quarter of it has 16384 registers and takes every fourth warp.
+int ctas_per_sm(int threads, int regs) {
+  const int warps = 16384 / (32 * regs), each = (threads / 32 + 3) / 4;
+  return std::max(1, std::min(warps / each, 2048 / threads));
+}
 
 }  // namespace
 
@@ -140,16 +153,18 @@ int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t
   p.eps = eps;
   const int vecs = static_cast<int>((channels + 7) / 8);
   // Few rows: as many threads a row as there are vectors, latency counts.
-  // Many: four vectors a thread, so that a multiprocessor holds several rows
-  // whose loads and reductions overlap.
-  int kv = rows <= sms ? (vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4) : 4;
-  if (vecs > 4096) kv = 0;
+  // Many: four vectors a thread and the next row loaded ahead.
+  const bool few = rows <= sms;
+  const int kv = vecs > 2048 ? 0 : !few ? 4 : vecs <= 1024 ? 1 : 2;
   int row_threads = kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
-  const int rows_cta = std::max(1, (rows <= sms ? 32 : 256) / row_threads);
-  Kernel k = kv == 0 ? kernel_of<0>(format) : kv == 1 ? kernel_of<1>(format) : kv == 2 ? kernel_of<2>(format) : kernel_of<4>(format);
+  const bool ahead = kv && !few;
+  const int rows_cta = ahead ? std::max(1, 128 / row_threads) : 1;
+  const int64_t need = (rows + rows_cta - 1) / rows_cta;
+  const int64_t grid =
+      ahead ? std::min<int64_t>(need, int64_t{sms} * ctas_per_sm(row_threads * rows_cta, sdq::norm::kAheadRegs)) : need;
   void* args[] = {&p, &row_threads};
-  return launch(reinterpret_cast<const void*>(k), dim3(static_cast<unsigned>((rows + rows_cta - 1) / rows_cta)),
-                dim3(row_threads * rows_cta), static_cast<cudaStream_t>(stream), args);
+  return launch(kernel_for(format, kv, ahead), dim3(static_cast<unsigned>(grid)), dim3(row_threads * rows_cta),
+                static_cast<cudaStream_t>(stream), args);
 }
 
 size_t sdq_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t channels) {
@@ -211,9 +226,9 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
   const int vecs = static_cast<int>((channels + 7) / 8);
   const int kv = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
   const int threads = kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
-  const int per_sm = std::max(1, std::min(4, (kv == 4 ? 512 : 1024) / threads));
+  const int per_sm = kv ? std::min(4, ctas_per_sm(threads, sdq::norm::backward_regs(kv))) : 1;
   p.parts = static_cast<int32_t>(std::min<int64_t>(rows, std::min<int64_t>(kMaxParts, int64_t{sms} * per_sm)));
-  void (*k)(BwdParams) = kv == 0   ? sdq::norm::rmsnorm_backward_kernel<0>
+  void (*k)(BwdParams) = kv == 0   ? sdq::norm::rmsnorm_backward_long_kernel
                          : kv == 1 ? sdq::norm::rmsnorm_backward_kernel<1>
                          : kv == 2 ? sdq::norm::rmsnorm_backward_kernel<2>
                                    : sdq::norm::rmsnorm_backward_kernel<4>;

@@ -68,63 +68,84 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, int row_w
   return __reduce_max_sync(0xffffffffu, lane < row_warps ? red[first + lane] : 0u);
 }
 
-__device__ __forceinline__ void load_weight8(const Params& p, int32_t k, float (&w)[8]) {
-  if (p.weight_f32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p.weight + 4 * static_cast<int64_t>(k)));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p.weight + 4 * static_cast<int64_t>(k)) + 1);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+// Eight weights from channel k on.
+__device__ __forceinline__ void load_weight8(const uint8_t* weight, int f32, int32_t k, float2 (&w)[4]) {
+  if (f32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(weight + 4 * k));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(weight + 4 * k) + 1);
+    w[0] = make_float2(a.x, a.y);
+    w[1] = make_float2(a.z, a.w);
+    w[2] = make_float2(b.x, b.y);
+    w[3] = make_float2(b.z, b.w);
   } else {
-    quant::unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight + 2 * static_cast<int64_t>(k))), w);
+    quant::unpack8(__ldg(reinterpret_cast<const uint4*>(weight + 2 * k)), w);
   }
 }
 
-__device__ __forceinline__ uint4 load_h8(const Params& p, int64_t row, int32_t k) {
-  uint4 a = *reinterpret_cast<const uint4*>(p.x + 2 * (row * p.ld_x + k));
-  if (p.residual) {
-    const uint4 b = *reinterpret_cast<const uint4*>(p.residual + 2 * (row * p.ld_residual + k));
-    float f[8], r[8];
-    quant::unpack8(a, f);
-    quant::unpack8(b, r);
-    a = make_uint4(pack_bf16x2(f[0] + r[0], f[1] + r[1]), pack_bf16x2(f[2] + r[2], f[3] + r[3]),
-                   pack_bf16x2(f[4] + r[4], f[5] + r[5]), pack_bf16x2(f[6] + r[6], f[7] + r[7]));
-    *reinterpret_cast<uint4*>(p.h + 2 * (row * p.ld_h + k)) = a;
-  }
-  return a;
-}
+// The rows of a call's arrays, so that a vector's address is one addition.
+struct Row {
+  const uint8_t *x, *r;
+  uint8_t *h, *q, *y;
+  __device__ __forceinline__ Row(const Params& p, int64_t row)
+      : x(p.x + 2 * row * p.ld_x),
+        r(p.residual ? p.residual + 2 * row * p.ld_residual : nullptr),
+        h(p.residual ? p.h + 2 * row * p.ld_h : nullptr),
+        q(p.q + row * p.ld_q),
+        y(p.y ? p.y + 2 * row * p.ld_y : nullptr) {}
+};
 
-__device__ __forceinline__ float sumsq8(const uint4& a) {
-  float f[8], s = 0.0f;
-  quant::unpack8(a, f);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
+// x and residual as they lie in memory, and h from them.
+struct Raw8 {
+  uint4 x, r;
+};
+__device__ __forceinline__ Raw8 load_raw8(const uint8_t* x, const uint8_t* r, int32_t k) {
+  Raw8 v;
+  v.x = *reinterpret_cast<const uint4*>(x + 2 * k);
+  if (r) v.r = *reinterpret_cast<const uint4*>(r + 2 * k);
+  return v;
+}
+// The sum of two bf16 numbers rounded once is what rounding it to fp32 first
+// gives: where fp32 would drop bits, the smaller number lies 2^8 below the
+// spacing of bf16 and cannot reach a tie.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint4 make_h8(uint8_t* h, int32_t k, const Raw8& v) {
+  if (!h) return v.x;
+  const uint4 s = make_uint4(add_bf16x2(v.x.x, v.r.x), add_bf16x2(v.x.y, v.r.y), add_bf16x2(v.x.z, v.r.z),
+                             add_bf16x2(v.x.w, v.r.w));
+  *reinterpret_cast<uint4*>(h + 2 * k) = s;
   return s;
 }
 
-__device__ __forceinline__ uint32_t norm8(const Params& p, const uint4& a, int32_t k, float rstd, float (&y)[8]) {
-  float w[8];
-  load_weight8(p, k, w);
-  quant::unpack8(a, y);
-  uint32_t m = 0;
+__device__ __forceinline__ float sumsq8(const uint4& a) {
+  float2 f[4], s = make_float2(0.0f, 0.0f);
+  quant::unpack8(a, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    y[i] = __fmul_rn(__fmul_rn(y[i], rstd), w[i]);
-    m = max(m, quant::mag(y[i]));
-  }
-  return m;
+  for (int i = 0; i < 4; ++i) s = __ffma2_rn(f[i], f[i], s);
+  return s.x + s.y;
+}
+
+// y of eight channels, and the largest magnitude among them.
+__device__ __forceinline__ uint32_t norm8(const Params& p, const uint4& a, int32_t k, float rstd, float2 (&y)[4]) {
+  float2 w[4];
+  load_weight8(p.weight, p.weight_f32, k, w);
+  quant::unpack8(a, y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(y[i], make_float2(rstd, rstd)), w[i]);
+  return quant::amax8(y);
 }
 
 template <Codes C, Scales S>
-__device__ __forceinline__ void store8(const Params& p, int64_t row, int32_t k, const float (&y)[8],
-                                       const quant::GroupScale& g) {
+__device__ __forceinline__ void store8(const Row& r, int32_t k, const float2 (&y)[4], const quant::GroupScale& g) {
   const uint2 c = quant::codes8<C, S>(y, g);
   if (C == Codes::kE2M1)
-    *reinterpret_cast<uint32_t*>(p.q + row * p.ld_q + (k >> 1)) = c.x;
+    *reinterpret_cast<uint32_t*>(r.q + (k >> 1)) = c.x;
   else
-    *reinterpret_cast<uint2*>(p.q + row * p.ld_q + k) = c;
-  if (p.y)
-    *reinterpret_cast<uint4*>(p.y + 2 * (row * p.ld_y + k)) =
-        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    *reinterpret_cast<uint2*>(r.q + k) = c;
+  if (r.y) *reinterpret_cast<uint4*>(r.y + 2 * k) = quant::pack8(y);
 }
 
 template <Codes C, Scales S>
@@ -140,76 +161,157 @@ __device__ __forceinline__ void store_scale(const Params& p, int64_t row, int32_
 // Threads [0, row_threads) of a CTA take its first row, and so on.  A thread
 // holds vectors of 8 consecutive channels, the next thread the next 8, so a
 // group of 16 to 256 channels is 2 to 32 neighbouring lanes of a warp.
-// kVecs > 0: the row is in registers, kVecs vectors a thread.  kVecs = 0: any
-// length, h read again (from L2) for the second pass and, with a scale per
-// row, for a third.
-template <Codes C, Scales S, int kVecs>
-__global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(const Params p, int row_threads) {
-  __shared__ float red[2][32];
+
+// The codes and scales of vector k of a row whose rstd is known.  rg: the scale
+// of the whole row (group 0), else set here.
+template <Codes C, Scales S>
+__device__ __forceinline__ void finish8(const Params& p, const Row& r, int64_t row, int32_t k, bool act, int t,
+                                        const uint4& h, float rstd, float g, quant::GroupScale& rg) {
+  constexpr int kFixed = C != Codes::kE2M1 ? 0 : S == Scales::kE8M0 ? 32 : 16;   // E2M1: the format's group
+  float2 y[4] = {};
+  uint32_t m = 0;
+  if (act) m = norm8(p, h, k, rstd, y);
+  if (kFixed || p.group != 0) {
+    const int lanes = (kFixed ? kFixed : p.group) >> 3;   // lanes of a group
+    if (kFixed) {
+#pragma unroll
+      for (int d = 1; d < kFixed / 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    } else {
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));   // 32 channels at least
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      if (lanes > 4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+      if (lanes > 8) m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      if (lanes > 16) m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    }
+    rg = quant::group_scale<C, S>(m, g);
+    if (act && (t & (lanes - 1)) == 0) store_scale<C, S>(p, row, (k >> 3) / lanes, rg);
+  }
+  if (act) store8<C, S>(r, k, y, rg);
+}
+
+__device__ __forceinline__ float rstd_of(const Params& p, float ss) {
+  return __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(p.channels)) + p.eps);
+}
+
+// Groups that pad the last scale tile: zero, as the product multiplies them
+// with zero codes.
+template <Codes C>
+__device__ __forceinline__ void pad_scales(const Params& p, int64_t row, int t) {
+  if (C == Codes::kE2M1 && t < p.tiles_k * 4 - p.groups) p.s[quant::tiled_scale(row, p.groups + t, p.tiles_k)] = 0;
+}
+
+// Rows that fit the registers, kVecs vectors a thread.  With kAhead a
+// persistent grid, the loads of the next row under way while a row is
+// reduced, normed and stored: else a multiprocessor's loads come in bursts
+// with pauses between them.
+template <Codes C, Scales S, int kVecs, bool kAhead>
+__device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) {
+  __shared__ float red[2][2][32];
   grid_dependency_wait();   // inputs may come from the previous kernel in the stream
   grid_launch_dependents();
-  const int row_warps = row_threads >> 5;
+  const int row_warps = row_threads >> 5, rows_cta = blockDim.x / row_threads;
   const int t = threadIdx.x % row_threads;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / row_threads) + threadIdx.x / row_threads;
-  const bool on = row < p.rows;
   const float g = S == Scales::kE4M3 && p.global ? *p.global : 1.0f;
-  uint4 hv[kVecs > 0 ? kVecs : 1];
-  float ss = 0.0f;
-  if (kVecs > 0) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * rows_cta + threadIdx.x / row_threads;
+  Raw8 raw[kVecs];
+  auto load = [&](int64_t from) {
+    if (from >= p.rows) return;
+    const Row r(p, from);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if ((t + i * row_threads) * 8 < p.channels) raw[i] = load_raw8(r.x, r.r, (t + i * row_threads) * 8);
+  };
+  load(row);
+  int flip = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows_cta; base < p.rows; base += stride, row += stride) {
+    const bool on = row < p.rows;
+    const Row r(p, row);
+    uint4 hv[kVecs];
+    float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int k = (t + i * row_threads) * 8;
       hv[i] = make_uint4(0, 0, 0, 0);
       if (on && k < p.channels) {
-        hv[i] = load_h8(p, row, k);
+        hv[i] = make_h8(r.h, k, raw[i]);
         ss += sumsq8(hv[i]);
       }
     }
-  } else {
-    for (int k = t * 8; on && k < p.channels; k += row_threads * 8) ss += sumsq8(load_h8(p, row, k));
-  }
-  ss = row_sum(ss, red[0], row_warps);
-  const float rstd = __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(p.channels)) + p.eps);
-  if (on && t == 0 && p.rstd) p.rstd[row] = rstd;
-
-  const uint8_t* hb = p.residual ? p.h : p.x;
-  const int64_t ldh = p.residual ? p.ld_h : p.ld_x;
-  const int lanes = p.group >> 3;   // lanes of a group
-  const int steps = kVecs > 0 ? kVecs : (p.channels + row_threads * 8 - 1) / (row_threads * 8);
-  quant::GroupScale rg;
-  if (p.group == 0) {
-    uint32_t m = 0;
+    if (kAhead) load(row + stride);
+    ss = row_sum(ss, red[flip][0], row_warps);
+    const float rstd = rstd_of(p, ss);
+    if (on && t == 0 && p.rstd) p.rstd[row] = rstd;
+    quant::GroupScale rg;
+    if (C != Codes::kE2M1 && p.group == 0) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < (kVecs > 0 ? kVecs : steps); ++i) {
-      const int k = (t + i * row_threads) * 8;
-      if (on && k < p.channels) {
-        float y[8];
-        m = max(m, norm8(p, kVecs > 0 ? hv[kVecs > 0 ? i : 0] : *reinterpret_cast<const uint4*>(hb + 2 * (row * ldh + k)),
-                         k, rstd, y));
+      for (int i = 0; i < kVecs; ++i) {
+        const int k = (t + i * row_threads) * 8;
+        float2 y[4];
+        if (on && k < p.channels) m = max(m, norm8(p, hv[i], k, rstd, y));
       }
+      rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[flip][1]), row_warps), g);
+      if (on && t == 0) store_scale<C, S>(p, row, 0, rg);
     }
-    rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[1]), row_warps), g);
-    if (on && t == 0) store_scale<C, S>(p, row, 0, rg);
-  }
+    flip ^= 1;
 #pragma unroll
-  for (int i = 0; i < (kVecs > 0 ? kVecs : steps); ++i) {
-    const int k = (t + i * row_threads) * 8;
-    const bool act = on && k < p.channels;
-    float y[8] = {};
-    uint32_t m = 0;
-    if (act)
-      m = norm8(p, kVecs > 0 ? hv[kVecs > 0 ? i : 0] : *reinterpret_cast<const uint4*>(hb + 2 * (row * ldh + k)), k,
-                rstd, y);
-    if (p.group != 0) {
-      for (int d = 1; d < lanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      rg = quant::group_scale<C, S>(m, g);
-      if (act && (t & (lanes - 1)) == 0) store_scale<C, S>(p, row, k / p.group, rg);
+    for (int i = 0; i < kVecs; ++i) {
+      const int k = (t + i * row_threads) * 8;
+      finish8<C, S>(p, r, row, k, on && k < p.channels, t, hv[i], rstd, g, rg);
     }
-    if (act) store8<C, S>(p, row, k, y, rg);
+    if (on) pad_scales<C>(p, row, t);
+    if (!kAhead) break;   // one row a thread
   }
-  // groups that pad the last scale tile: zero, as the product multiplies them with zero codes
-  if (C == Codes::kE2M1 && on && t < p.tiles_k * 4 - p.groups)
-    p.s[quant::tiled_scale(row, p.groups + t, p.tiles_k)] = 0;
+}
+
+template <Codes C, Scales S, int kVecs>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(const Params p, int row_threads) {
+  rmsnorm_quant<C, S, kVecs, false>(p, row_threads);
+}
+
+// 80 registers: six warps a quarter of a multiprocessor.
+constexpr int kAheadVecs = 4, kAheadRegs = 80, kAheadThreads = 512;
+
+template <Codes C, Scales S>
+__global__ void __maxnreg__(kAheadRegs) rmsnorm_quant_rows_kernel(const Params p, int row_threads) {
+  rmsnorm_quant<C, S, kAheadVecs, true>(p, row_threads);
+}
+
+// Longer rows: h is read again (from L2) for the second pass, and with a scale
+// a row for a third.
+template <Codes C, Scales S>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_long_kernel(const Params p) {
+  __shared__ float red[2][32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int t = threadIdx.x, warps = blockDim.x >> 5, step = blockDim.x * 8;
+  const int64_t row = blockIdx.x;
+  const Row r(p, row);
+  const float g = S == Scales::kE4M3 && p.global ? *p.global : 1.0f;
+  float ss = 0.0f;
+  for (int k = t * 8; k < p.channels; k += step) ss += sumsq8(make_h8(r.h, k, load_raw8(r.x, r.r, k)));
+  ss = row_sum(ss, red[0], warps);
+  const float rstd = rstd_of(p, ss);
+  if (t == 0 && p.rstd) p.rstd[row] = rstd;
+  const uint8_t* h = r.h ? r.h : r.x;
+  quant::GroupScale rg;
+  if (C != Codes::kE2M1 && p.group == 0) {
+    uint32_t m = 0;
+    for (int k = t * 8; k < p.channels; k += step) {
+      float2 y[4];
+      m = max(m, norm8(p, *reinterpret_cast<const uint4*>(h + 2 * k), k, rstd, y));
+    }
+    rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[1]), warps), g);
+    if (t == 0) store_scale<C, S>(p, row, 0, rg);
+  }
+  for (int k0 = 0; k0 < p.channels; k0 += step) {
+    const int k = k0 + t * 8;
+    const bool act = k < p.channels;
+    finish8<C, S>(p, r, row, k, act, t, act ? *reinterpret_cast<const uint4*>(h + 2 * k) : make_uint4(0, 0, 0, 0), rstd,
+                  g, rg);
+  }
+  pad_scales<C>(p, row, t);
 }
 
 // ---- backward ---------------------------------------------------------------
@@ -227,93 +329,150 @@ struct BwdParams {
   int32_t channels, weight_f32, parts;
 };
 
-__device__ __forceinline__ void bwd_weight8(const BwdParams& p, int32_t k, float (&w)[8]) {
-  Params q;
-  q.weight = p.weight;
-  q.weight_f32 = p.weight_f32;
-  load_weight8(q, k, w);
-}
-
 // CTA b takes rows b, b + parts, ... and adds their grad_y n to its own row of
 // `part`, in that order; grad_weight_kernel adds the rows of `part` in theirs.
 // No atomics: the result does not depend on timing.
+
+// grad_x of eight channels, grad_y n of them added to acc.  c: rstd^3 times the
+// row's mean of grad_y w h.
+__device__ __forceinline__ void backward8(const BwdParams& p, uint8_t* gx, int32_t k, const uint4& gyv, const uint4& hv,
+                                          const uint4& ghv, float rstd, float c, float2 (&acc)[4]) {
+  float2 gy[4], h[4], gh[4], w[4];
+  quant::unpack8(gyv, gy);
+  quant::unpack8(hv, h);
+  quant::unpack8(ghv, gh);
+  load_weight8(p.weight, p.weight_f32, k, w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 r = make_float2(rstd, rstd);
+    const float2 o = __ffma2_rn(__fmul2_rn(gy[i], w[i]), r, gh[i]);
+    gh[i] = __ffma2_rn(h[i], make_float2(-c, -c), o);
+    acc[i] = __ffma2_rn(gy[i], __fmul2_rn(h[i], r), acc[i]);
+  }
+  *reinterpret_cast<uint4*>(gx + 2 * k) = quant::pack8(gh);
+}
+
+__device__ __forceinline__ float dot8(const BwdParams& p, int32_t k, const uint4& gyv, const uint4& hv) {
+  float2 gy[4], h[4], w[4], s = make_float2(0.0f, 0.0f);
+  quant::unpack8(gyv, gy);
+  quant::unpack8(hv, h);
+  load_weight8(p.weight, p.weight_f32, k, w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = __ffma2_rn(__fmul2_rn(gy[i], w[i]), h[i], s);
+  return s.x + s.y;
+}
+
+// rstd^3 mean(grad_y w h), from the row's sum.
+__device__ __forceinline__ float backward_factor(const BwdParams& p, float rstd, float dot) {
+  return rstd * rstd * (rstd * __fdiv_rn(dot, static_cast<float>(p.channels)));
+}
+
+// Rows that fit the registers, kVecs vectors a thread: grad_y and h of the next
+// row are loaded ahead, grad_h while the row's sum is added up.
 template <int kVecs>
-__global__ void __launch_bounds__(kVecs < 2 ? kMaxThreads : 512) rmsnorm_backward_kernel(const BwdParams p) {
+__device__ __forceinline__ void rmsnorm_backward(const BwdParams& p) {
   __shared__ float red[2][32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int t = threadIdx.x, threads = blockDim.x, warps = threads >> 5;
-  float acc[kVecs > 0 ? kVecs : 1][8] = {};
-  float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
-    const float rstd = p.rstd[row];
-    uint4 gv[kVecs > 0 ? kVecs : 1], hv[kVecs > 0 ? kVecs : 1];
-    float dot = 0.0f;
-    const int steps = kVecs > 0 ? kVecs : (p.channels + threads * 8 - 1) / (threads * 8);
-#pragma unroll
-    for (int i = 0; i < (kVecs > 0 ? kVecs : steps); ++i) {
-      const int k = (t + i * threads) * 8;
-      if (k < p.channels) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p.gy + 2 * (row * p.ld_gy + k));
-        const uint4 b = *reinterpret_cast<const uint4*>(p.h + 2 * (row * p.ld_h + k));
-        float gy[8], h[8], w[8];
-        quant::unpack8(a, gy);
-        quant::unpack8(b, h);
-        bwd_weight8(p, k, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dot = fmaf(gy[e] * w[e], h[e] * rstd, dot);
-        if (kVecs > 0) {
-          gv[kVecs > 0 ? i : 0] = a;
-          hv[kVecs > 0 ? i : 0] = b;
-        }
-      }
-    }
-    dot = row_sum(dot, red[flip], warps);
-    flip ^= 1;
-    const float c = __fdiv_rn(dot, static_cast<float>(p.channels));
-#pragma unroll
-    for (int i = 0; i < (kVecs > 0 ? kVecs : steps); ++i) {
-      const int k = (t + i * threads) * 8;
-      if (k < p.channels) {
-        const uint4 a = kVecs > 0 ? gv[kVecs > 0 ? i : 0] : *reinterpret_cast<const uint4*>(p.gy + 2 * (row * p.ld_gy + k));
-        const uint4 b = kVecs > 0 ? hv[kVecs > 0 ? i : 0] : *reinterpret_cast<const uint4*>(p.h + 2 * (row * p.ld_h + k));
-        float gy[8], h[8], w[8], o[8], r[8] = {};
-        quant::unpack8(a, gy);
-        quant::unpack8(b, h);
-        bwd_weight8(p, k, w);
-        if (p.gh) quant::unpack8(*reinterpret_cast<const uint4*>(p.gh + 2 * (row * p.ld_gh + k)), r);
-        float d[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = h[e] * rstd;
-          o[e] = fmaf(rstd, fmaf(-n, c, gy[e] * w[e]), r[e]);
-          d[e] = gy[e] * n;
-        }
-        *reinterpret_cast<uint4*>(p.gx + 2 * (row * p.ld_gx + k)) =
-            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-        if (kVecs > 0) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[kVecs > 0 ? i : 0][e] += d[e];
-        } else {   // the thread's own 8 sums, in memory
-          float4* q = reinterpret_cast<float4*>(part + k);
-          float4 u = make_float4(0, 0, 0, 0), v = u;
-          if (row != blockIdx.x) { u = q[0]; v = q[1]; }
-          q[0] = make_float4(u.x + d[0], u.y + d[1], u.z + d[2], u.w + d[3]);
-          q[1] = make_float4(v.x + d[4], v.y + d[5], v.z + d[6], v.w + d[7]);
-        }
-      }
-    }
-  }
-  if (kVecs > 0) {
+  float2 acc[kVecs][4] = {};
+  uint4 gn[kVecs], hn[kVecs];
+  auto load = [&](int64_t row) {
+    if (row >= p.rows) return;
+    const uint8_t* gy = p.gy + 2 * row * p.ld_gy;
+    const uint8_t* h = p.h + 2 * row * p.ld_h;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int k = (t + i * threads) * 8;
       if (k < p.channels) {
-        float4* q = reinterpret_cast<float4*>(part + k);
-        q[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        q[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+        gn[i] = *reinterpret_cast<const uint4*>(gy + 2 * k);
+        hn[i] = *reinterpret_cast<const uint4*>(h + 2 * k);
       }
+    }
+  };
+  load(blockIdx.x);
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
+    const float rstd = p.rstd[row];
+    const uint8_t* gh = p.gh ? p.gh + 2 * row * p.ld_gh : nullptr;
+    uint8_t* gx = p.gx + 2 * row * p.ld_gx;
+    uint4 gv[kVecs], hv[kVecs], rv[kVecs];
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int k = (t + i * threads) * 8;
+      gv[i] = gn[i];
+      hv[i] = hn[i];
+      rv[i] = make_uint4(0, 0, 0, 0);
+      if (k < p.channels) {
+        if (gh) rv[i] = *reinterpret_cast<const uint4*>(gh + 2 * k);
+        dot += dot8(p, k, gv[i], hv[i]);
+      }
+    }
+    load(row + p.parts);
+    dot = row_sum(dot, red[flip], warps);
+    flip ^= 1;
+    const float c = backward_factor(p, rstd, dot);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int k = (t + i * threads) * 8;
+      if (k < p.channels) backward8(p, gx, k, gv[i], hv[i], rv[i], rstd, c, acc[i]);
+    }
+  }
+  float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int k = (t + i * threads) * 8;
+    if (k < p.channels) {
+      float4* q = reinterpret_cast<float4*>(part + k);
+      q[0] = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+      q[1] = make_float4(acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y);
+    }
+  }
+}
+
+// Registers a thread, and with them warps a quarter of a multiprocessor: 8, 6, 4.
+constexpr int backward_regs(int vecs) { return vecs == 1 ? 64 : vecs == 2 ? 80 : 128; }
+
+template <int kVecs>
+__global__ void __maxnreg__(backward_regs(kVecs)) rmsnorm_backward_kernel(const BwdParams p) {
+  rmsnorm_backward<kVecs>(p);
+}
+
+// Longer rows: read twice, the sums of grad_y n in memory between rows (a
+// thread's own).
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_long_kernel(const BwdParams p) {
+  __shared__ float red[2][32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int t = threadIdx.x, warps = blockDim.x >> 5, step = blockDim.x * 8;
+  float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
+    const float rstd = p.rstd[row];
+    const uint8_t *gy = p.gy + 2 * row * p.ld_gy, *h = p.h + 2 * row * p.ld_h;
+    const uint8_t* gh = p.gh ? p.gh + 2 * row * p.ld_gh : nullptr;
+    uint8_t* gx = p.gx + 2 * row * p.ld_gx;
+    float dot = 0.0f;
+    for (int k = t * 8; k < p.channels; k += step)
+      dot += dot8(p, k, *reinterpret_cast<const uint4*>(gy + 2 * k), *reinterpret_cast<const uint4*>(h + 2 * k));
+    dot = row_sum(dot, red[flip], warps);
+    flip ^= 1;
+    const float c = backward_factor(p, rstd, dot);
+    for (int k = t * 8; k < p.channels; k += step) {
+      float4* q = reinterpret_cast<float4*>(part + k);
+      float2 acc[4] = {};
+      if (row != blockIdx.x) {
+        const float4 u = q[0], v = q[1];
+        acc[0] = make_float2(u.x, u.y);
+        acc[1] = make_float2(u.z, u.w);
+        acc[2] = make_float2(v.x, v.y);
+        acc[3] = make_float2(v.z, v.w);
+      }
+      backward8(p, gx, k, *reinterpret_cast<const uint4*>(gy + 2 * k), *reinterpret_cast<const uint4*>(h + 2 * k),
+                gh ? *reinterpret_cast<const uint4*>(gh + 2 * k) : make_uint4(0, 0, 0, 0), rstd, c, acc);
+      q[0] = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
+      q[1] = make_float4(acc[2].x, acc[2].y, acc[3].x, acc[3].y);
     }
   }
 }

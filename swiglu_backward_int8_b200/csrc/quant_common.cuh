@@ -13,8 +13,13 @@
 //   scale 1.  A group that holds a NaN or an infinity has a NaN scale (fp32
 //   NaN, E8M0 0xFF, E4M3 0x7F) and zero codes, so all of it reads back as NaN.
 //
-// Magnitudes are compared as unsigned bit patterns with the sign cleared: the
-// order is that of the numbers, infinities and NaN above all finite ones.
+// A group's largest magnitude travels as its bits with the sign cleared: their
+// unsigned order is that of the numbers, infinities and NaN above all finite
+// ones.
+//
+// These kernels move few bytes a value, so instructions bound them as soon as
+// there are about 15 a value: pairs of values go through two-wide fp32
+// instructions, quotients are products with a reciprocal and one Newton step.
 #pragma once
 
 #include <cstdint>
@@ -34,7 +39,44 @@ __host__ __device__ constexpr float qmax() {
   return C == Codes::kInt8 ? 127.0f : C == Codes::kE4M3 ? 448.0f : 6.0f;
 }
 
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// The largest of three magnitudes; a NaN if one of them is.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t amax8(const float2 (&y)[4]) {
+  float m = amax3(0.0f, y[0].x, y[0].y);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = amax3(m, y[i].x, y[i].y);
+  return __float_as_uint(m);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+}
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                    pack_bf16x2(f[3].x, f[3].y));
+}
+
+// 1 / u within an ulp of the rounded reciprocal, for u and 1 / u normal.
+__device__ __forceinline__ float reciprocal(float u) {
+  const float r = rcp_approx(u);
+  return fmaf(fmaf(-u, r, 1.0f), r, r);
+}
+
+// a / kQ for a constant kQ, correctly rounded: the remainder of the product with
+// the rounded reciprocal is exact while it does not underflow.
+template <int kQ>
+__device__ __forceinline__ float quotient(float a) {
+  constexpr float kInv = 1.0f / kQ;
+  if (a < 1e-30f) return __fdiv_rn(a, static_cast<float>(kQ));
+  const float q = __fmul_rn(a, kInv);
+  return fmaf(fmaf(-q, static_cast<float>(kQ), a), kInv, q);
+}
 
 // 2^k for -127 <= k <= 127 (2^-127 is subnormal).
 __device__ __forceinline__ float exp2i(int k) {
@@ -61,7 +103,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
 
 // Eight floats -> eight E2M1 codes (nearest even, saturated to 6), the first
 // in the low four bits.  cvt puts its first source in the upper half.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -70,7 +112,7 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
       "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
       "mov.b32 %0, {a, b, c, d};\n}\n"
       : "=r"(r)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
   return r;
 }
 
@@ -101,12 +143,12 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float g) {
   if (S == Scales::kF32) {
     // at least the smallest subnormal, so that a code times the scale stays
     // near the value however small the group is
-    r.scale = amax_bits ? fmaxf(__fdiv_rn(amax, qmax<C>()), __uint_as_float(1u)) : 1.0f;
+    r.scale = amax_bits ? fmaxf(quotient<static_cast<int>(qmax<C>())>(amax), __uint_as_float(1u)) : 1.0f;
     r.unit = r.scale;
-    r.inv = __frcp_rn(r.unit);
+    r.inv = reciprocal(r.unit);
     if (r.unit < 1.17549435e-38f) r.mode = 1;   // below 2^-126 the reciprocal may overflow
   } else if (S == Scales::kE8M0) {
-    const int k = amax_bits ? ceil_exp(__fdiv_rn(amax, qmax<C>())) : 0;
+    const int k = amax_bits ? ceil_exp(quotient<static_cast<int>(qmax<C>())>(amax)) : 0;
     r.byte = static_cast<uint32_t>(k + 127);
     r.scale = r.unit = exp2i(k);
     r.inv = exp2i(-k);                          // both exact: no rounding before the code's
@@ -115,67 +157,59 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float g) {
     if (r.byte == 0) r.byte = 1;                // 2^-9: a group this small still has codes
     r.scale = e4m3_value(r.byte);
     r.unit = __fmul_rn(r.scale, g);
-    r.inv = __frcp_rn(r.unit);
+    r.inv = reciprocal(r.unit);
     if (!(r.unit > 7.9e-31f && r.unit < 1.2e30f)) r.mode = 1;   // outside 2^+-100
   }
   return r;
 }
 
+// v * inv rounded to whole numbers by one fused multiply-add each (quant_bits).
+__device__ __forceinline__ uint2 int8x8(const float2 (&v)[4], float inv) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = __ffma2_rn(v[i], make_float2(inv, inv), make_float2(12582912.0f, 12582912.0f));
+    b[2 * i] = __float_as_uint(q.x);
+    b[2 * i + 1] = __float_as_uint(q.y);
+  }
+  return make_uint2(pack_low_bytes(b[0], b[1], b[2], b[3]), pack_low_bytes(b[4], b[5], b[6], b[7]));
+}
+
 // Eight values -> codes: two words of bytes (INT8, E4M3) or one word (E2M1).
 template <Codes C, Scales S>
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], const GroupScale& g) {
-  float v[8];
+__device__ __forceinline__ uint2 codes8(const float2 (&y)[4], const GroupScale& g) {
+  if (g.mode == 2) return make_uint2(0u, 0u);
+  float2 v[4];
   if (g.mode == 0) {
+    if (C == Codes::kInt8) return int8x8(y, g.inv);
+    const float2 inv = make_float2(g.inv, g.inv);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (C == Codes::kInt8) {
-        v[i] = y[i];
-      } else if (C == Codes::kE2M1 && S == Scales::kE4M3) {
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __fmul2_rn(y[i], inv);
+      if (C == Codes::kE2M1 && S == Scales::kE4M3) {
         // the quotient y / unit correctly rounded: one Newton step on the
-        // product with the rounded reciprocal.  Values and scales of few bits
-        // meet exact ties, which the product alone would miss.  (With the
-        // signs this way round a zero keeps its own.)
-        const float q = __fmul_rn(y[i], g.inv);
-        v[i] = fmaf(-fmaf(q, g.unit, -y[i]), g.inv, q);
-      } else {
-        v[i] = __fmul_rn(y[i], g.inv);
+        // product with the reciprocal.  Values and scales of few bits meet exact
+        // ties, which the product alone would miss.  (With the signs this way
+        // round a zero keeps its own.)
+        const float2 rem = __ffma2_rn(v[i], make_float2(g.unit, g.unit), make_float2(-y[i].x, -y[i].y));
+        v[i] = __ffma2_rn(make_float2(-rem.x, -rem.y), inv, v[i]);
       }
     }
-    if (C == Codes::kInt8) {
-      uint32_t b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = quant_bits(v[i], g.inv);
-      return make_uint2(pack_low_bytes(b[0], b[1], b[2], b[3]), pack_low_bytes(b[4], b[5], b[6], b[7]));
-    }
-  } else if (g.mode == 1) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(__fdiv_rn(y[i], g.unit), -qmax<C>()), qmax<C>());
-    if (C == Codes::kInt8) {
-      uint32_t b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = quant_bits(v[i], 1.0f);
-      return make_uint2(pack_low_bytes(b[0], b[1], b[2], b[3]), pack_low_bytes(b[4], b[5], b[6], b[7]));
-    }
   } else {
-    return make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(fminf(fmaxf(__fdiv_rn(y[i].x, g.unit), -qmax<C>()), qmax<C>()),
+                         fminf(fmaxf(__fdiv_rn(y[i].y, g.unit), -qmax<C>()), qmax<C>()));
+    if (C == Codes::kInt8) return int8x8(v, 1.0f);
   }
   if (C == Codes::kE2M1) return make_uint2(e2m1x8(v), 0u);
-  return make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+  return make_uint2(e4m3x4(v[0].x, v[0].y, v[1].x, v[1].y), e4m3x4(v[2].x, v[2].y, v[3].x, v[3].y));
 }
 
 // Byte offset of the scale of (row, group) in the tiled layout the product
 // reads: tiles of 128 rows x 4 groups, `tiles_k` of them side by side.
 __device__ __forceinline__ int64_t tiled_scale(int64_t row, int32_t group, int32_t tiles_k) {
   return ((row >> 7) * tiles_k + (group >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (group & 3);
-}
-
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
 }
 
 }  // namespace quant
