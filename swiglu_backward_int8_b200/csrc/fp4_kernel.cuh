@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
   const int64_t m0 = static_cast<int64_t>(tile_m) * kTile;
   const int nrows = static_cast<int>(min(static_cast<int64_t>(kTile), p.rows - m0));
   const int nch = min(kTile, p.channels - k0);
-  const float g = S == Scales::kE4M3 && p.global ? *p.global : 1.0f;
+  const quant::Divisor g = quant::divisor<Codes::kE2M1, S>(p.global);
   const int c8 = (t & 15) * 8;
 #pragma unroll
   for (int i = 0; i < kTile * 16 / kThreads; ++i) {
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
     if (kRows) {
       float2 y[4];
       quant::unpack8(v, y);
-      uint32_t m = quant::amax8(y);
+      uint32_t m = quant::amax(y);
 #pragma unroll
       for (int d = 1; d < G / 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
       const quant::GroupScale gs = quant::group_scale<Codes::kE2M1, S>(m, g);

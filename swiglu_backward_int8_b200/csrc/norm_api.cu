@@ -16,24 +16,22 @@ using sdq::norm::Params;
 using sdq::quant::Codes;
 using sdq::quant::Scales;
 
-// The kernel for a format: one or two vectors a thread for a row, four with the
-// next row loaded ahead, or (vecs 0) the one for long rows.
+enum class Variant { kFew, kMany, kLong };
+
 template <Codes C, Scales S>
-const void* kernel_of(int vecs, bool ahead) {
-  using sdq::norm::rmsnorm_quant_kernel;
-  if (vecs == 0) return reinterpret_cast<const void*>(sdq::norm::rmsnorm_quant_long_kernel<C, S>);
-  if (ahead) return reinterpret_cast<const void*>(sdq::norm::rmsnorm_quant_rows_kernel<C, S>);
-  return vecs == 1 ? reinterpret_cast<const void*>(rmsnorm_quant_kernel<C, S, 1>)
-                   : reinterpret_cast<const void*>(rmsnorm_quant_kernel<C, S, 2>);
+const void* kernel_of(Variant v) {
+  return v == Variant::kFew    ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_quant_kernel<C, S>)
+         : v == Variant::kMany ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_quant_rows_kernel<C, S>)
+                               : reinterpret_cast<const void*>(sdq::norm::rmsnorm_quant_long_kernel<C, S>);
 }
 
-const void* kernel_for(uint32_t format, int vecs, bool ahead) {
+const void* kernel_for(uint32_t format, Variant v) {
   const bool e8 = format & SDQ_FMT_E8M0;
   if (format & SDQ_FMT_E2M1)
-    return e8 ? kernel_of<Codes::kE2M1, Scales::kE8M0>(vecs, ahead) : kernel_of<Codes::kE2M1, Scales::kE4M3>(vecs, ahead);
+    return e8 ? kernel_of<Codes::kE2M1, Scales::kE8M0>(v) : kernel_of<Codes::kE2M1, Scales::kE4M3>(v);
   if (format & SDQ_FMT_E4M3)
-    return e8 ? kernel_of<Codes::kE4M3, Scales::kE8M0>(vecs, ahead) : kernel_of<Codes::kE4M3, Scales::kF32>(vecs, ahead);
-  return e8 ? kernel_of<Codes::kInt8, Scales::kE8M0>(vecs, ahead) : kernel_of<Codes::kInt8, Scales::kF32>(vecs, ahead);
+    return e8 ? kernel_of<Codes::kE4M3, Scales::kE8M0>(v) : kernel_of<Codes::kE4M3, Scales::kF32>(v);
+  return e8 ? kernel_of<Codes::kInt8, Scales::kE8M0>(v) : kernel_of<Codes::kInt8, Scales::kF32>(v);
 }
 
 constexpr uint32_t kFormatBits = SDQ_FMT_E4M3 | SDQ_FMT_E8M0 | SDQ_FMT_E2M1 | SDQ_FMT_SCALE_E4M3 | SDQ_FMT_WEIGHT_F32;
@@ -151,19 +149,20 @@ int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t
   p.tiles_k = (groups + 3) / 4;
   p.weight_f32 = format & SDQ_FMT_WEIGHT_F32 ? 1 : 0;
   p.eps = eps;
-  const int vecs = static_cast<int>((channels + 7) / 8);
-  // Few rows: as many threads a row as there are vectors, latency counts.
-  // Many: four vectors a thread and the next row loaded ahead.
-  const bool few = rows <= sms;
-  const int kv = vecs > 2048 ? 0 : !few ? 4 : vecs <= 1024 ? 1 : 2;
-  int row_threads = kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
-  const bool ahead = kv && !few;
-  const int rows_cta = ahead ? std::max(1, 128 / row_threads) : 1;
-  const int64_t need = (rows + rows_cta - 1) / rows_cta;
-  const int64_t grid =
-      ahead ? std::min<int64_t>(need, int64_t{sms} * ctas_per_sm(row_threads * rows_cta, sdq::norm::kAheadRegs)) : need;
+  const int vecs = static_cast<int>(channels / sdq::norm::kVec);
+  // Few rows: a vector a thread, latency counts.  Many: two, and the next row
+  // loaded ahead.  Rows that neither holds: read again.
+  const Variant v = rows <= sms && vecs <= sdq::norm::kMaxThreads               ? Variant::kFew
+                    : vecs <= sdq::norm::kAheadThreads * sdq::norm::kAheadVecs ? Variant::kMany
+                                                                               : Variant::kLong;
+  const int each = v == Variant::kMany ? sdq::norm::kAheadVecs : 1;
+  int row_threads = v == Variant::kLong ? sdq::norm::kMaxThreads : round_up((vecs + each - 1) / each, 32);
+  const int rows_cta = v == Variant::kMany ? std::max(1, 128 / row_threads) : 1;
+  int64_t grid = (rows + rows_cta - 1) / rows_cta;
+  if (v == Variant::kMany)
+    grid = std::min<int64_t>(grid, int64_t{sms} * ctas_per_sm(row_threads * rows_cta, sdq::norm::kAheadRegs));
   void* args[] = {&p, &row_threads};
-  return launch(kernel_for(format, kv, ahead), dim3(static_cast<unsigned>(grid)), dim3(row_threads * rows_cta),
+  return launch(kernel_for(format, v), dim3(static_cast<unsigned>(grid)), dim3(row_threads * rows_cta),
                 static_cast<cudaStream_t>(stream), args);
 }
 

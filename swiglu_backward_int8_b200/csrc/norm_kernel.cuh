@@ -68,42 +68,51 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, int row_w
   return __reduce_max_sync(0xffffffffu, lane < row_warps ? red[first + lane] : 0u);
 }
 
-// Eight weights from channel k on.
-__device__ __forceinline__ void load_weight8(const uint8_t* weight, int f32, int32_t k, float2 (&w)[4]) {
+// A vector of 16 channels: as loaded, and as 8 pairs of numbers.  (With 8
+// channels a vector the addresses, checks and scales took 35 instructions a
+// channel, more than the loads' time.)
+constexpr int kVec = 16;
+struct Vec {
+  uint4 a, b;
+};
+__device__ __forceinline__ Vec load_vec(const uint8_t* p, int32_t k) {
+  const uint4* q = reinterpret_cast<const uint4*>(p + 2 * k);
+  return {q[0], q[1]};
+}
+__device__ __forceinline__ void store_vec(uint8_t* p, int32_t k, const Vec& v) {
+  uint4* q = reinterpret_cast<uint4*>(p + 2 * k);
+  q[0] = v.a;
+  q[1] = v.b;
+}
+using Pairs = float2[8];
+__device__ __forceinline__ void unpack(const Vec& v, Pairs& f) {
+  const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+}
+__device__ __forceinline__ Vec pack(const Pairs& f) {
+  return {make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                     pack_bf16x2(f[3].x, f[3].y)),
+          make_uint4(pack_bf16x2(f[4].x, f[4].y), pack_bf16x2(f[5].x, f[5].y), pack_bf16x2(f[6].x, f[6].y),
+                     pack_bf16x2(f[7].x, f[7].y))};
+}
+
+// The weights from channel k on.
+__device__ __forceinline__ void load_weight(const uint8_t* weight, int f32, int32_t k, Pairs& w) {
   if (f32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(weight + 4 * k));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(weight + 4 * k) + 1);
-    w[0] = make_float2(a.x, a.y);
-    w[1] = make_float2(a.z, a.w);
-    w[2] = make_float2(b.x, b.y);
-    w[3] = make_float2(b.z, b.w);
+    const float4* q = reinterpret_cast<const float4*>(weight + 4 * k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = __ldg(q + i);
+      w[2 * i] = make_float2(v.x, v.y);
+      w[2 * i + 1] = make_float2(v.z, v.w);
+    }
   } else {
-    quant::unpack8(__ldg(reinterpret_cast<const uint4*>(weight + 2 * k)), w);
+    const uint4* q = reinterpret_cast<const uint4*>(weight + 2 * k);
+    unpack({__ldg(q), __ldg(q + 1)}, w);
   }
 }
 
-// The rows of a call's arrays, so that a vector's address is one addition.
-struct Row {
-  const uint8_t *x, *r;
-  uint8_t *h, *q, *y;
-  __device__ __forceinline__ Row(const Params& p, int64_t row)
-      : x(p.x + 2 * row * p.ld_x),
-        r(p.residual ? p.residual + 2 * row * p.ld_residual : nullptr),
-        h(p.residual ? p.h + 2 * row * p.ld_h : nullptr),
-        q(p.q + row * p.ld_q),
-        y(p.y ? p.y + 2 * row * p.ld_y : nullptr) {}
-};
-
-// x and residual as they lie in memory, and h from them.
-struct Raw8 {
-  uint4 x, r;
-};
-__device__ __forceinline__ Raw8 load_raw8(const uint8_t* x, const uint8_t* r, int32_t k) {
-  Raw8 v;
-  v.x = *reinterpret_cast<const uint4*>(x + 2 * k);
-  if (r) v.r = *reinterpret_cast<const uint4*>(r + 2 * k);
-  return v;
-}
 // The sum of two bf16 numbers rounded once is what rounding it to fp32 first
 // gives: where fp32 would drop bits, the smaller number lies 2^8 below the
 // spacing of bf16 and cannot reach a tie.
@@ -112,40 +121,40 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint4 make_h8(uint8_t* h, int32_t k, const Raw8& v) {
-  if (!h) return v.x;
-  const uint4 s = make_uint4(add_bf16x2(v.x.x, v.r.x), add_bf16x2(v.x.y, v.r.y), add_bf16x2(v.x.z, v.r.z),
-                             add_bf16x2(v.x.w, v.r.w));
-  *reinterpret_cast<uint4*>(h + 2 * k) = s;
-  return s;
+__device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
+  return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
 }
 
-__device__ __forceinline__ float sumsq8(const uint4& a) {
-  float2 f[4], s = make_float2(0.0f, 0.0f);
-  quant::unpack8(a, f);
+__device__ __forceinline__ float sumsq(const Vec& v) {
+  Pairs f;
+  float2 s = make_float2(0.0f, 0.0f);
+  unpack(v, f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s = __ffma2_rn(f[i], f[i], s);
+  for (int i = 0; i < 8; ++i) s = __ffma2_rn(f[i], f[i], s);
   return s.x + s.y;
 }
 
-// y of eight channels, and the largest magnitude among them.
-__device__ __forceinline__ uint32_t norm8(const Params& p, const uint4& a, int32_t k, float rstd, float2 (&y)[4]) {
-  float2 w[4];
-  load_weight8(p.weight, p.weight_f32, k, w);
-  quant::unpack8(a, y);
+// y of 16 channels, and the largest magnitude among them.
+__device__ __forceinline__ uint32_t norm_vec(const Params& p, const Vec& h, int32_t k, float rstd, Pairs& y) {
+  Pairs w;
+  load_weight(p.weight, p.weight_f32, k, w);
+  unpack(h, y);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(y[i], make_float2(rstd, rstd)), w[i]);
-  return quant::amax8(y);
+  for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(__fmul2_rn(y[i], make_float2(rstd, rstd)), w[i]);
+  return quant::amax(y);
 }
 
 template <Codes C, Scales S>
-__device__ __forceinline__ void store8(const Row& r, int32_t k, const float2 (&y)[4], const quant::GroupScale& g) {
-  const uint2 c = quant::codes8<C, S>(y, g);
+__device__ __forceinline__ void store_codes(const Params& p, int64_t row, int32_t k, const Pairs& y,
+                                            const quant::GroupScale& g) {
+  const uint2 a = quant::codes8<C, S>(*reinterpret_cast<const float2(*)[4]>(&y[0]), g);
+  const uint2 b = quant::codes8<C, S>(*reinterpret_cast<const float2(*)[4]>(&y[4]), g);
+  uint8_t* q = p.q + row * p.ld_q;
   if (C == Codes::kE2M1)
-    *reinterpret_cast<uint32_t*>(r.q + (k >> 1)) = c.x;
+    *reinterpret_cast<uint2*>(q + (k >> 1)) = make_uint2(a.x, b.x);
   else
-    *reinterpret_cast<uint2*>(r.q + k) = c;
-  if (r.y) *reinterpret_cast<uint4*>(r.y + 2 * k) = quant::pack8(y);
+    *reinterpret_cast<uint4*>(q + k) = make_uint4(a.x, a.y, b.x, b.y);
+  if (p.y) store_vec(p.y + 2 * row * p.ld_y, k, pack(y));
 }
 
 template <Codes C, Scales S>
@@ -159,34 +168,33 @@ __device__ __forceinline__ void store_scale(const Params& p, int64_t row, int32_
 }
 
 // Threads [0, row_threads) of a CTA take its first row, and so on.  A thread
-// holds vectors of 8 consecutive channels, the next thread the next 8, so a
-// group of 16 to 256 channels is 2 to 32 neighbouring lanes of a warp.
+// holds vectors of 16 consecutive channels, the next thread the next 16, so a
+// group of 16 to 256 channels is 1 to 16 neighbouring lanes of a warp.
 
 // The codes and scales of vector k of a row whose rstd is known.  rg: the scale
 // of the whole row (group 0), else set here.
 template <Codes C, Scales S>
-__device__ __forceinline__ void finish8(const Params& p, const Row& r, int64_t row, int32_t k, bool act, int t,
-                                        const uint4& h, float rstd, float g, quant::GroupScale& rg) {
-  constexpr int kFixed = C != Codes::kE2M1 ? 0 : S == Scales::kE8M0 ? 32 : 16;   // E2M1: the format's group
-  float2 y[4] = {};
+__device__ __forceinline__ void finish(const Params& p, int64_t row, int32_t k, bool act, int t, const Vec& h, float rstd,
+                                       const quant::Divisor& d, quant::GroupScale& rg) {
+  Pairs y = {};
   uint32_t m = 0;
-  if (act) m = norm8(p, h, k, rstd, y);
-  if (kFixed || p.group != 0) {
-    const int lanes = (kFixed ? kFixed : p.group) >> 3;   // lanes of a group
-    if (kFixed) {
-#pragma unroll
-      for (int d = 1; d < kFixed / 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    } else {
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));   // 32 channels at least
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  if (act) m = norm_vec(p, h, k, rstd, y);
+  if (C == Codes::kE2M1 || p.group != 0) {
+    int lanes = 1;   // of a group
+    if (C != Codes::kE2M1 || S == Scales::kE8M0) {   // 32 channels at least
+      lanes = 2;
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    }
+    if (C != Codes::kE2M1) {
+      lanes = p.group >> 4;
+      if (lanes > 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       if (lanes > 4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
       if (lanes > 8) m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
-      if (lanes > 16) m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
     }
-    rg = quant::group_scale<C, S>(m, g);
-    if (act && (t & (lanes - 1)) == 0) store_scale<C, S>(p, row, (k >> 3) / lanes, rg);
+    rg = quant::group_scale<C, S>(m, d);
+    if (act && (t & (lanes - 1)) == 0) store_scale<C, S>(p, row, (k >> 4) / lanes, rg);
   }
-  if (act) store8<C, S>(r, k, y, rg);
+  if (act) store_codes<C, S>(p, row, k, y, rg);
 }
 
 __device__ __forceinline__ float rstd_of(const Params& p, float ss) {
@@ -211,31 +219,38 @@ __device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) 
   grid_launch_dependents();
   const int row_warps = row_threads >> 5, rows_cta = blockDim.x / row_threads;
   const int t = threadIdx.x % row_threads;
-  const float g = S == Scales::kE4M3 && p.global ? *p.global : 1.0f;
+  const quant::Divisor d = quant::divisor<C, S>(p.global);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
   int64_t row = static_cast<int64_t>(blockIdx.x) * rows_cta + threadIdx.x / row_threads;
-  Raw8 raw[kVecs];
+  Vec x[kVecs], r[kVecs];
   auto load = [&](int64_t from) {
     if (from >= p.rows) return;
-    const Row r(p, from);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if ((t + i * row_threads) * 8 < p.channels) raw[i] = load_raw8(r.x, r.r, (t + i * row_threads) * 8);
+    for (int i = 0; i < kVecs; ++i) {
+      const int k = (t + i * row_threads) * kVec;
+      if (k < p.channels) {
+        x[i] = load_vec(p.x + 2 * from * p.ld_x, k);
+        if (p.residual) r[i] = load_vec(p.residual + 2 * from * p.ld_residual, k);
+      }
+    }
   };
   load(row);
   int flip = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows_cta; base < p.rows; base += stride, row += stride) {
     const bool on = row < p.rows;
-    const Row r(p, row);
-    uint4 hv[kVecs];
+    Vec h[kVecs];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int k = (t + i * row_threads) * 8;
-      hv[i] = make_uint4(0, 0, 0, 0);
+      const int k = (t + i * row_threads) * kVec;
+      h[i] = {};
       if (on && k < p.channels) {
-        hv[i] = make_h8(r.h, k, raw[i]);
-        ss += sumsq8(hv[i]);
+        h[i] = x[i];
+        if (p.residual) {
+          h[i] = {add_bf16x8(x[i].a, r[i].a), add_bf16x8(x[i].b, r[i].b)};
+          store_vec(p.h + 2 * row * p.ld_h, k, h[i]);
+        }
+        ss += sumsq(h[i]);
       }
     }
     if (kAhead) load(row + stride);
@@ -247,31 +262,32 @@ __device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) 
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
-        const int k = (t + i * row_threads) * 8;
-        float2 y[4];
-        if (on && k < p.channels) m = max(m, norm8(p, hv[i], k, rstd, y));
+        const int k = (t + i * row_threads) * kVec;
+        Pairs y;
+        if (on && k < p.channels) m = max(m, norm_vec(p, h[i], k, rstd, y));
       }
-      rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[flip][1]), row_warps), g);
+      rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[flip][1]), row_warps), d);
       if (on && t == 0) store_scale<C, S>(p, row, 0, rg);
     }
     flip ^= 1;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int k = (t + i * row_threads) * 8;
-      finish8<C, S>(p, r, row, k, on && k < p.channels, t, hv[i], rstd, g, rg);
+      const int k = (t + i * row_threads) * kVec;
+      finish<C, S>(p, row, k, on && k < p.channels, t, h[i], rstd, d, rg);
     }
     if (on) pad_scales<C>(p, row, t);
     if (!kAhead) break;   // one row a thread
   }
 }
 
-template <Codes C, Scales S, int kVecs>
+// Few rows: one vector a thread.
+template <Codes C, Scales S>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(const Params p, int row_threads) {
-  rmsnorm_quant<C, S, kVecs, false>(p, row_threads);
+  rmsnorm_quant<C, S, 1, false>(p, row_threads);
 }
 
 // 80 registers: six warps a quarter of a multiprocessor.
-constexpr int kAheadVecs = 4, kAheadRegs = 80, kAheadThreads = 512;
+constexpr int kAheadVecs = 2, kAheadRegs = 80, kAheadThreads = 512;
 
 template <Codes C, Scales S>
 __global__ void __maxnreg__(kAheadRegs) rmsnorm_quant_rows_kernel(const Params p, int row_threads) {
@@ -285,31 +301,37 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_long_kernel(const P
   __shared__ float red[2][32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = threadIdx.x, warps = blockDim.x >> 5, step = blockDim.x * 8;
+  const int t = threadIdx.x, warps = blockDim.x >> 5, step = blockDim.x * kVec;
   const int64_t row = blockIdx.x;
-  const Row r(p, row);
-  const float g = S == Scales::kE4M3 && p.global ? *p.global : 1.0f;
+  const quant::Divisor d = quant::divisor<C, S>(p.global);
+  const uint8_t* hb = p.residual ? p.h + 2 * row * p.ld_h : p.x + 2 * row * p.ld_x;
   float ss = 0.0f;
-  for (int k = t * 8; k < p.channels; k += step) ss += sumsq8(make_h8(r.h, k, load_raw8(r.x, r.r, k)));
+  for (int k = t * kVec; k < p.channels; k += step) {
+    Vec h = load_vec(p.x + 2 * row * p.ld_x, k);
+    if (p.residual) {
+      const Vec r = load_vec(p.residual + 2 * row * p.ld_residual, k);
+      h = {add_bf16x8(h.a, r.a), add_bf16x8(h.b, r.b)};
+      store_vec(p.h + 2 * row * p.ld_h, k, h);
+    }
+    ss += sumsq(h);
+  }
   ss = row_sum(ss, red[0], warps);
   const float rstd = rstd_of(p, ss);
   if (t == 0 && p.rstd) p.rstd[row] = rstd;
-  const uint8_t* h = r.h ? r.h : r.x;
   quant::GroupScale rg;
   if (C != Codes::kE2M1 && p.group == 0) {
     uint32_t m = 0;
-    for (int k = t * 8; k < p.channels; k += step) {
-      float2 y[4];
-      m = max(m, norm8(p, *reinterpret_cast<const uint4*>(h + 2 * k), k, rstd, y));
+    for (int k = t * kVec; k < p.channels; k += step) {
+      Pairs y;
+      m = max(m, norm_vec(p, load_vec(hb, k), k, rstd, y));
     }
-    rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[1]), warps), g);
+    rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[1]), warps), d);
     if (t == 0) store_scale<C, S>(p, row, 0, rg);
   }
   for (int k0 = 0; k0 < p.channels; k0 += step) {
-    const int k = k0 + t * 8;
+    const int k = k0 + t * kVec;
     const bool act = k < p.channels;
-    finish8<C, S>(p, r, row, k, act, t, act ? *reinterpret_cast<const uint4*>(h + 2 * k) : make_uint4(0, 0, 0, 0), rstd,
-                  g, rg);
+    finish<C, S>(p, row, k, act, t, act ? load_vec(hb, k) : Vec{}, rstd, d, rg);
   }
   pad_scales<C>(p, row, t);
 }
@@ -332,6 +354,19 @@ struct BwdParams {
 // CTA b takes rows b, b + parts, ... and adds their grad_y n to its own row of
 // `part`, in that order; grad_weight_kernel adds the rows of `part` in theirs.
 // No atomics: the result does not depend on timing.
+
+__device__ __forceinline__ void load_weight8(const uint8_t* weight, int f32, int32_t k, float2 (&w)[4]) {
+  if (f32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(weight + 4 * k));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(weight + 4 * k) + 1);
+    w[0] = make_float2(a.x, a.y);
+    w[1] = make_float2(a.z, a.w);
+    w[2] = make_float2(b.x, b.y);
+    w[3] = make_float2(b.z, b.w);
+  } else {
+    quant::unpack8(__ldg(reinterpret_cast<const uint4*>(weight + 2 * k)), w);
+  }
+}
 
 // grad_x of eight channels, grad_y n of them added to acc.  c: rstd^3 times the
 // row's mean of grad_y w h.

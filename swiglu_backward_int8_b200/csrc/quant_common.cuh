@@ -45,10 +45,11 @@ __device__ __forceinline__ float amax3(float a, float b, float c) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t amax8(const float2 (&y)[4]) {
+template <int kPairs>
+__device__ __forceinline__ uint32_t amax(const float2 (&y)[kPairs]) {
   float m = amax3(0.0f, y[0].x, y[0].y);
 #pragma unroll
-  for (int i = 1; i < 4; ++i) m = amax3(m, y[i].x, y[i].y);
+  for (int i = 1; i < kPairs; ++i) m = amax3(m, y[i].x, y[i].y);
   return __float_as_uint(m);
 }
 
@@ -68,14 +69,11 @@ __device__ __forceinline__ float reciprocal(float u) {
   return fmaf(fmaf(-u, r, 1.0f), r, r);
 }
 
-// a / kQ for a constant kQ, correctly rounded: the remainder of the product with
-// the rounded reciprocal is exact while it does not underflow.
-template <int kQ>
-__device__ __forceinline__ float quotient(float a) {
-  constexpr float kInv = 1.0f / kQ;
-  if (a < 1e-30f) return __fdiv_rn(a, static_cast<float>(kQ));
-  const float q = __fmul_rn(a, kInv);
-  return fmaf(fmaf(-q, static_cast<float>(kQ), a), kInv, q);
+// a / d correctly rounded, with inv near 1 / d: the remainder of the product is
+// exact while it does not underflow.
+__device__ __forceinline__ float quotient(float a, float d, float inv) {
+  const float q = __fmul_rn(a, inv);
+  return fmaf(fmaf(-q, d, a), inv, q);
 }
 
 // 2^k for -127 <= k <= 127 (2^-127 is subnormal).
@@ -116,6 +114,20 @@ __device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
   return r;
 }
 
+// What the groups of a call share: the divisor of a group's largest magnitude,
+// its reciprocal, and the scale per tensor.
+struct Divisor {
+  float d, inv, g;
+};
+template <Codes C, Scales S>
+__device__ __forceinline__ Divisor divisor(const float* global) {
+  Divisor v;
+  v.g = S == Scales::kE4M3 && global ? *global : 1.0f;
+  v.d = S == Scales::kE4M3 ? __fmul_rn(6.0f, v.g) : qmax<C>();
+  v.inv = S == Scales::kE4M3 ? __frcp_rn(v.d) : 1.0f / qmax<C>();
+  return v;
+}
+
 // How a group's values become codes.
 struct GroupScale {
   float scale;     // as stored (fp32 scales), or the number behind `byte`
@@ -125,9 +137,9 @@ struct GroupScale {
   int mode;        // 0: multiply by inv; 1: divide by unit (inv may overflow); 2: not finite
 };
 
-// amax_bits: the group's largest magnitude; g: the scale per tensor (E4M3 scales).
+// Any group: zero, tiny, huge, not finite.
 template <Codes C, Scales S>
-__device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float g) {
+__device__ __noinline__ GroupScale group_scale_any(uint32_t amax_bits, Divisor v) {
   GroupScale r;
   r.byte = 0;
   if (amax_bits >= kInfBits) {
@@ -143,22 +155,52 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, float g) {
   if (S == Scales::kF32) {
     // at least the smallest subnormal, so that a code times the scale stays
     // near the value however small the group is
-    r.scale = amax_bits ? fmaxf(quotient<static_cast<int>(qmax<C>())>(amax), __uint_as_float(1u)) : 1.0f;
+    r.scale = amax_bits ? fmaxf(__fdiv_rn(amax, v.d), __uint_as_float(1u)) : 1.0f;
     r.unit = r.scale;
-    r.inv = reciprocal(r.unit);
+    r.inv = __frcp_rn(r.unit);
     if (r.unit < 1.17549435e-38f) r.mode = 1;   // below 2^-126 the reciprocal may overflow
   } else if (S == Scales::kE8M0) {
-    const int k = amax_bits ? ceil_exp(quotient<static_cast<int>(qmax<C>())>(amax)) : 0;
+    const int k = amax_bits ? ceil_exp(__fdiv_rn(amax, v.d)) : 0;
     r.byte = static_cast<uint32_t>(k + 127);
     r.scale = r.unit = exp2i(k);
     r.inv = exp2i(-k);                          // both exact: no rounding before the code's
   } else {
-    r.byte = amax_bits ? e4m3_byte(__fdiv_rn(amax, __fmul_rn(6.0f, g))) : 0x38u;
+    r.byte = amax_bits ? e4m3_byte(__fdiv_rn(amax, v.d)) : 0x38u;
     if (r.byte == 0) r.byte = 1;                // 2^-9: a group this small still has codes
     r.scale = e4m3_value(r.byte);
-    r.unit = __fmul_rn(r.scale, g);
-    r.inv = reciprocal(r.unit);
+    r.unit = __fmul_rn(r.scale, v.g);
+    r.inv = __frcp_rn(r.unit);
     if (!(r.unit > 7.9e-31f && r.unit < 1.2e30f)) r.mode = 1;   // outside 2^+-100
+  }
+  return r;
+}
+
+// amax_bits: the group's largest magnitude.  Between 2^-90 and 2^90 no step
+// leaves the normal range.
+template <Codes C, Scales S>
+__device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, const Divisor& v) {
+  constexpr uint32_t kLow = (127u - 90u) << 23, kHigh = (127u + 90u) << 23;
+  // (a scale per tensor may be anything: its units are looked at too)
+  const bool usual = amax_bits - kLow < kHigh - kLow && (S != Scales::kE4M3 || (v.g > 1e-18f && v.g < 1e18f));
+  if (!usual) return group_scale_any<C, S>(amax_bits, v);
+  GroupScale r;
+  r.byte = 0;
+  r.mode = 0;
+  const float t = quotient(__uint_as_float(amax_bits), v.d, v.inv);
+  if (S == Scales::kF32) {
+    r.scale = r.unit = t;
+    r.inv = reciprocal(t);
+  } else if (S == Scales::kE8M0) {
+    r.byte = (__float_as_uint(t) + 0x7FFFFFu) >> 23;   // the exponent, one more where the mantissa is not zero
+    r.scale = r.unit = __uint_as_float(r.byte << 23);
+    r.inv = __uint_as_float((254u - r.byte) << 23);
+  } else {
+    r.byte = max(e4m3_byte(t), 1u);
+    uint32_t h;
+    asm("{\n\t.reg .b16 b;\n\tcvt.u16.u32 b, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n}\n" : "=r"(h) : "r"(r.byte));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n}\n" : "=f"(r.scale) : "r"(h));
+    r.unit = __fmul_rn(r.scale, v.g);
+    r.inv = reciprocal(r.unit);
   }
   return r;
 }
