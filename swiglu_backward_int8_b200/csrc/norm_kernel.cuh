@@ -286,8 +286,9 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(const Params
   rmsnorm_quant<C, S, 1, false>(p, row_threads);
 }
 
-// 80 registers: six warps a quarter of a multiprocessor.
-constexpr int kAheadVecs = 2, kAheadRegs = 80, kAheadThreads = 512;
+// One vector a thread, 64 registers: eight warps a quarter of a multiprocessor
+// (two vectors and 80 registers, six warps: 160 us where this takes 138).
+constexpr int kAheadVecs = 1, kAheadRegs = 64, kAheadThreads = 1024;
 
 template <Codes C, Scales S>
 __global__ void __maxnreg__(kAheadRegs) rmsnorm_quant_rows_kernel(const Params p, int row_threads) {
