@@ -221,6 +221,7 @@ int sdq_validate_dequantize_fp4(const void* q, int64_t ld_q, const void* s, cons
                                 int64_t ld_out, int64_t rows, int64_t channels, uint32_t format) {
   if (!format_ok(format)) return SDQ_ERR_FORMAT;
   if (rows < 0 || rows > SDQ_MAX_M || !length_ok(channels)) return SDQ_ERR_SHAPE;
+  if ((rows + 31) / 32 * ((channels + 255) / 256) > INT32_MAX) return SDQ_ERR_SHAPE;   // tiles of the grid
   if (rows == 0) return SDQ_OK;
   if (!q || !s || !out) return SDQ_ERR_NULL;
   if (ld_q < channels / 2 || ld_q > SDQ_MAX_LD || ld_out < channels || ld_out > SDQ_MAX_LD) return SDQ_ERR_STRIDE;
@@ -234,8 +235,6 @@ int sdq_dequantize_fp4(const void* q, int64_t ld_q, const void* s, const float* 
                        int64_t rows, int64_t channels, uint32_t format, void* stream) {
   const int st = sdq_validate_dequantize_fp4(q, ld_q, s, global_scale, out, ld_out, rows, channels, format);
   if (st != SDQ_OK || rows == 0) return st;
-  int sms = 0;
-  if (const int e = sdq_internal::sm_count(&sms)) return e;
   sdq::fp4::DequantParams p = {};
   p.q = static_cast<const uint8_t*>(q);
   p.s = static_cast<const uint8_t*>(s);
@@ -246,11 +245,12 @@ int sdq_dequantize_fp4(const void* q, int64_t ld_q, const void* s, const float* 
   p.ld_out = ld_out;
   p.channels = static_cast<int32_t>(channels);
   p.tiles_k = static_cast<int32_t>(tiles_of(channels, format));
-  const int64_t need = (rows * (channels / 8) + sdq::fp4::kThreads - 1) / sdq::fp4::kThreads;
+  constexpr int kRows = sdq::fp4::kThreads / 32 * sdq::fp4::kDequantRows;
+  p.grid_k = static_cast<int32_t>((channels + sdq::fp4::kDequantCols - 1) / sdq::fp4::kDequantCols);
   void* args[] = {&p};
   return launch(format & SDQ_FMT_E8M0 ? reinterpret_cast<const void*>(sdq::fp4::dequantize_kernel<Scales::kE8M0>)
                                       : reinterpret_cast<const void*>(sdq::fp4::dequantize_kernel<Scales::kE4M3>),
-                static_cast<unsigned>(std::min<int64_t>(need, int64_t{sms} * 8)), sdq::fp4::kThreads, 0,
+                static_cast<unsigned>((rows + kRows - 1) / kRows * p.grid_k), sdq::fp4::kThreads, 0,
                 static_cast<cudaStream_t>(stream), args);
 }
 

@@ -1,12 +1,15 @@
 // Microscaled 4-bit quantization (quant_common.cuh) of bf16 arrays along the
 // rows, along the columns (transposed), or both in one pass, and back.
 //
-// A CTA takes a tile of 128 rows x 128 channels.  Along the rows a thread has 8
-// consecutive channels of a row (a group is 4 or 2 neighbouring lanes); along
-// the columns a thread has one group of rows of two neighbouring channels,
-// read back from the tile in shared memory.  The scales of a tile are whole
-// 512-byte scale tiles (128 rows x 4 groups, or the transposed ones), put
-// together in shared memory.
+// A CTA takes a tile of 128 rows x 128 channels.  Along the rows a thread has 16
+// consecutive channels of a row (a group is one lane or two); along the columns
+// it has one group of rows of two neighbouring channels, read back from the tile
+// in shared memory, and the codes go through shared memory once more so that the
+// stores fill 64 bytes of a row.  The scales of a tile are whole 512-byte scale
+// tiles (128 rows x 4 groups, or the transposed ones), put together in shared
+// memory.
+//
+// 2 bytes are read and 0.53 or 0.56 written a value and axis; DRAM bounds it.
 #pragma once
 
 #include <cstdint>
@@ -37,13 +40,28 @@ struct QuantParams {
   int64_t tiles_m;         // scale tiles along the rows (of st)
 };
 
+// The scale tiles of a tile, from shared memory: word w of one has the four groups
+// of row (w / 4) + 32 (w % 4).  Rows past the last are left alone.
+template <int kAtoms>
+__device__ __forceinline__ void store_scale_tiles(const uint8_t* sc, uint8_t* out, int64_t first, int64_t last, int rows,
+                                                  int t) {
+  for (int w = t; w < kAtoms * 128; w += kThreads) {
+    const int r = ((w & 127) >> 2) + 32 * (w & 3);
+    const int64_t tile = first + (w >> 7);
+    if (r < rows && tile < last)
+      *reinterpret_cast<uint32_t*>(out + tile * 512 + (w & 127) * 4) = reinterpret_cast<const uint32_t*>(sc)[w];
+  }
+}
+
 template <Scales S, bool kRows, bool kCols>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, 3) quantize_kernel(const QuantParams p) {
   constexpr int G = S == Scales::kE8M0 ? 32 : 16;
   constexpr int kGroups = kTile / G;          // groups of a tile along either axis
   constexpr int kAtoms = kGroups / 4;         // scale tiles of a tile
   constexpr int kPitch = kTile * 2 + 16;      // bytes of a row of the tile
+  constexpr int kCodePitch = kTile / 2 + 16;  // bytes of a channel's codes
   __shared__ alignas(16) uint8_t tile[kCols ? kTile * kPitch : 16];
+  __shared__ alignas(16) uint8_t ct[kCols ? kTile * kCodePitch : 16];
   __shared__ alignas(16) uint8_t sc[kRows ? kAtoms * 512 : 16], sct[kCols ? kAtoms * 512 : 16];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -53,39 +71,45 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
   const int64_t m0 = static_cast<int64_t>(tile_m) * kTile;
   const int nrows = static_cast<int>(min(static_cast<int64_t>(kTile), p.rows - m0));
   const int nch = min(kTile, p.channels - k0);
-  const quant::Divisor g = quant::divisor<Codes::kE2M1, S>(p.global);
-  const int c8 = (t & 15) * 8;
+  const quant::Divisor d = quant::divisor<Codes::kE2M1, S>(p.global);
+  const int c16 = (t & 7) * 16;
+  constexpr int kStep = kThreads / 8, kPasses = kTile / kStep;   // rows of a pass
+  uint4 va[kPasses], vb[kPasses];
 #pragma unroll
-  for (int i = 0; i < kTile * 16 / kThreads; ++i) {
-    const int r = (t >> 4) + i * (kThreads / 16);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    const bool act = r < nrows && c8 < nch;
-    if (act) v = *reinterpret_cast<const uint4*>(p.x + 2 * ((m0 + r) * p.ld_x + k0 + c8));
-    if (kCols) *reinterpret_cast<uint4*>(tile + r * kPitch + c8 * 2) = v;
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = (t >> 3) + i * kStep;
+    va[i] = vb[i] = make_uint4(0, 0, 0, 0);
+    if (r < nrows && c16 < nch) {
+      const uint4* q = reinterpret_cast<const uint4*>(p.x + 2 * ((m0 + r) * p.ld_x + k0 + c16));
+      va[i] = q[0];
+      vb[i] = q[1];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = (t >> 3) + i * kStep;
+    if (kCols) {
+      *reinterpret_cast<uint4*>(tile + r * kPitch + c16 * 2) = va[i];
+      *reinterpret_cast<uint4*>(tile + r * kPitch + c16 * 2 + 16) = vb[i];
+    }
     if (kRows) {
-      float2 y[4];
-      quant::unpack8(v, y);
-      uint32_t m = quant::amax(y);
-#pragma unroll
-      for (int d = 1; d < G / 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const quant::GroupScale gs = quant::group_scale<Codes::kE2M1, S>(m, g);
-      if (act) *reinterpret_cast<uint32_t*>(p.q + (m0 + r) * p.ld_q + ((k0 + c8) >> 1)) = quant::codes8<Codes::kE2M1, S>(y, gs).x;
-      const int grp = c8 / G;
-      if ((c8 & (G - 1)) == 0)
-        sc[(grp >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (grp & 3)] = static_cast<uint8_t>(c8 < nch ? gs.byte : 0u);
+      float2 y[4], z[4];
+      quant::unpack8(va[i], y);
+      quant::unpack8(vb[i], z);
+      uint32_t m = max(quant::amax(y), quant::amax(z));
+      if (G == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      const quant::GroupScale gs = quant::group_scale<Codes::kE2M1, S>(m, d);
+      if (r < nrows && c16 < nch)
+        *reinterpret_cast<uint2*>(p.q + (m0 + r) * p.ld_q + ((k0 + c16) >> 1)) =
+            make_uint2(quant::codes8<Codes::kE2M1, S>(y, gs).x, quant::codes8<Codes::kE2M1, S>(z, gs).x);
+      const int grp = c16 / G;
+      if ((c16 & (G - 1)) == 0)
+        sc[(grp >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (grp & 3)] = static_cast<uint8_t>(c16 < nch ? gs.byte : 0u);
     }
   }
   __syncthreads();
-  if (kRows) {
-    // word w of a scale tile: the four groups of row (w / 4) + 32 (w % 4)
-    for (int w = t; w < kAtoms * 128; w += kThreads) {
-      const int atom = w >> 7, r = ((w & 127) >> 2) + 32 * (w & 3);
-      const int tk = tile_k * kAtoms + atom;
-      if (r < nrows && tk < p.tiles_k)
-        *reinterpret_cast<uint32_t*>(p.s + (static_cast<int64_t>(tile_m) * p.tiles_k + tk) * 512 + (w & 127) * 4) =
-            reinterpret_cast<const uint32_t*>(sc)[w];
-    }
-  }
+  if (kRows)
+    store_scale_tiles<kAtoms>(sc, p.s + static_cast<int64_t>(tile_m) * p.tiles_k * 512, tile_k * kAtoms, p.tiles_k, nrows, t);
   if (kCols) {
     const int c = (t & 63) * 2;                 // two channels
 #pragma unroll
@@ -100,42 +124,33 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
         ma = quant::amax3(ma, bf16_lo(v[e]), bf16_lo(v[e + 1]));
         mb = quant::amax3(mb, bf16_hi(v[e]), bf16_hi(v[e + 1]));
       }
-      const quant::GroupScale ga = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(ma), g);
-      const quant::GroupScale gb = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(mb), g);
-      const int64_t row = m0 + grp * G;
-      const bool in = row < p.rows_padded;      // whole groups: rows_padded is a multiple of 32
-      uint32_t qa[G / 8], qb[G / 8];
+      const quant::GroupScale ga = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(ma), d);
+      const quant::GroupScale gb = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(mb), d);
+      const bool in = m0 + grp * G < p.rows_padded;      // whole groups: rows_padded is a multiple of 32
 #pragma unroll
       for (int w = 0; w < G / 8; ++w) {
         float2 y[4];
+        uint8_t* o = ct + c * kCodePitch + grp * (G / 2) + w * 4;
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = make_float2(bf16_lo(v[w * 8 + 2 * e]), bf16_lo(v[w * 8 + 2 * e + 1]));
-        qa[w] = quant::codes8<Codes::kE2M1, S>(y, ga).x;
+        *reinterpret_cast<uint32_t*>(o) = quant::codes8<Codes::kE2M1, S>(y, ga).x;
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = make_float2(bf16_hi(v[w * 8 + 2 * e]), bf16_hi(v[w * 8 + 2 * e + 1]));
-        qb[w] = quant::codes8<Codes::kE2M1, S>(y, gb).x;
-      }
-      if (in && c < nch) {
-        uint8_t* d = p.qt + (k0 + c) * p.ld_qt + (row >> 1);
-        if (G == 32) {
-          *reinterpret_cast<uint4*>(d) = make_uint4(qa[0], qa[1], qa[G / 8 - 2], qa[G / 8 - 1]);
-          *reinterpret_cast<uint4*>(d + p.ld_qt) = make_uint4(qb[0], qb[1], qb[G / 8 - 2], qb[G / 8 - 1]);
-        } else {
-          *reinterpret_cast<uint2*>(d) = make_uint2(qa[0], qa[1]);
-          *reinterpret_cast<uint2*>(d + p.ld_qt) = make_uint2(qb[0], qb[1]);
-        }
+        *reinterpret_cast<uint32_t*>(o + kCodePitch) = quant::codes8<Codes::kE2M1, S>(y, gb).x;
       }
       uint8_t* o = sct + (grp >> 2) * 512 + (grp & 3);
       o[(c & 31) * 16 + (c >> 5) * 4] = static_cast<uint8_t>(in ? ga.byte : 0u);
       o[((c + 1) & 31) * 16 + (c >> 5) * 4] = static_cast<uint8_t>(in ? gb.byte : 0u);
     }
     __syncthreads();
-    for (int w = t; w < kAtoms * 128; w += kThreads) {
-      const int atom = w >> 7, r = ((w & 127) >> 2) + 32 * (w & 3);
-      const int64_t tm = static_cast<int64_t>(tile_m) * kAtoms + atom;
-      if (r < nch && tm < p.tiles_m)
-        *reinterpret_cast<uint32_t*>(p.st + (static_cast<int64_t>(tile_k) * p.tiles_m + tm) * 512 + (w & 127) * 4) =
-            reinterpret_cast<const uint32_t*>(sct)[w];
+    store_scale_tiles<kAtoms>(sct, p.st + static_cast<int64_t>(tile_k) * p.tiles_m * 512,
+                              static_cast<int64_t>(tile_m) * kAtoms, p.tiles_m, nch, t);
+#pragma unroll
+    for (int i = 0; i < kTile * 4 / kThreads; ++i) {   // 32 rows of a channel: 16 bytes
+      const int ch = (t >> 2) + i * (kThreads / 4), part = t & 3;
+      if (ch < nch && m0 + part * 32 < p.rows_padded)
+        *reinterpret_cast<uint4*>(p.qt + (k0 + ch) * p.ld_qt + (m0 >> 1) + part * 16) =
+            *reinterpret_cast<const uint4*>(ct + ch * kCodePitch + part * 16);
     }
   }
 }
@@ -149,19 +164,40 @@ struct DequantParams {
   uint8_t* out;            // bf16 rows, ld_out elements apart
   int64_t rows, ld_q, ld_out;
   int32_t channels, tiles_k;
+  int32_t grid_k;          // strips of 256 channels
 };
 
-// The value behind a code: a table lookup in registers (twice the magnitude
-// is a nibble of 0x C864 3210), exact; times the unit it is rounded once to
-// fp32 and once to bf16.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const float v = static_cast<float>((0xC8643210u >> ((c & 7u) * 4)) & 15u) * 0.5f;
-  return (c & 8u) ? -v : v;
+// Four codes pairs -> eight numbers: two codes of a byte become two fp16 numbers in
+// one instruction, exact; times the unit they are rounded once to fp32 and once
+// to bf16.
+__device__ __forceinline__ uint4 values8(uint32_t w, float unit) {
+  uint32_t h[4], o[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 f;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n}\n"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h[i]));
+    f = __fmul2_rn(f, make_float2(unit, unit));
+    o[i] = pack_bf16x2(f.x, f.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-__device__ __forceinline__ float e8m0_value(uint32_t b) {
-  return b == 255 ? __uint_as_float(0x7FC00000u) : quant::exp2i(static_cast<int>(b) - 127);
+// What a code of 1 stands for, from a scale's byte.
+template <Scales S>
+__device__ __forceinline__ float unit_of(uint32_t b, float g) {
+  if (S == Scales::kE8M0) return b == 255 ? __uint_as_float(0x7FC00000u) : quant::exp2i(static_cast<int>(b) - 127);
+  return (b & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : __fmul_rn(quant::e4m3_value(b), g);
 }
+
+// A warp takes 256 channels of kDequantRows rows, a lane 8 of them.
+constexpr int kDequantRows = 4, kDequantCols = 256;
 
 template <Scales S>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantParams p) {
@@ -169,25 +205,22 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantParam
   grid_dependency_wait();
   grid_launch_dependents();
   const float g = S == Scales::kE4M3 && p.global ? *p.global : 1.0f;
-  const int64_t vecs = p.channels >> 3;
-  const int64_t total = p.rows * vecs;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t row = i / vecs;
-    const int32_t k = static_cast<int32_t>(i - row * vecs) * 8;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p.q + row * p.ld_q + (k >> 1));
-    const uint32_t b = p.s[quant::tiled_scale(row, k / G, p.tiles_k)];
-    float unit;
-    if (S == Scales::kE8M0)
-      unit = e8m0_value(b);
-    else
-      unit = (b & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : __fmul_rn(quant::e4m3_value(b), g);
-    uint32_t o[4];
+  const int strip = blockIdx.x / p.grid_k;
+  const int k = (blockIdx.x - strip * p.grid_k) * kDequantCols + (threadIdx.x & 31) * 8;
+  const int64_t row0 = static_cast<int64_t>(strip) * (kThreads / 32 * kDequantRows) + (threadIdx.x >> 5) * kDequantRows;
+  if (k >= p.channels) return;
+  uint32_t w[kDequantRows], b[kDequantRows];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o[e] = pack_bf16x2(e2m1_value(w >> (8 * e)) * unit, e2m1_value(w >> (8 * e + 4)) * unit);
-    *reinterpret_cast<uint4*>(p.out + 2 * (row * p.ld_out + k)) = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int i = 0; i < kDequantRows; ++i) {
+    if (row0 + i < p.rows) {
+      w[i] = *reinterpret_cast<const uint32_t*>(p.q + (row0 + i) * p.ld_q + (k >> 1));
+      b[i] = p.s[quant::tiled_scale(row0 + i, k / G, p.tiles_k)];
+    }
   }
+#pragma unroll
+  for (int i = 0; i < kDequantRows; ++i)
+    if (row0 + i < p.rows)
+      *reinterpret_cast<uint4*>(p.out + 2 * ((row0 + i) * p.ld_out + k)) = values8(w[i], unit_of<S>(b[i], g));
 }
 
 }  // namespace fp4
