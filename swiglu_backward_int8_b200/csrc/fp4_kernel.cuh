@@ -54,12 +54,12 @@ __device__ __forceinline__ void store_scale_tiles(const uint8_t* sc, uint8_t* ou
 }
 
 template <Scales S, bool kRows, bool kCols>
-__global__ void __launch_bounds__(kThreads, 3) quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const QuantParams p) {
   constexpr int G = S == Scales::kE8M0 ? 32 : 16;
   constexpr int kGroups = kTile / G;          // groups of a tile along either axis
   constexpr int kAtoms = kGroups / 4;         // scale tiles of a tile
   constexpr int kPitch = kTile * 2 + 16;      // bytes of a row of the tile
-  constexpr int kCodePitch = kTile / 2 + 16;  // bytes of a channel's codes
+  constexpr int kCodePitch = kTile / 2;       // bytes of a channel's codes: four pieces of 16, swizzled by its number
   __shared__ alignas(16) uint8_t tile[kCols ? kTile * kPitch : 16];
   __shared__ alignas(16) uint8_t ct[kCols ? kTile * kCodePitch : 16];
   __shared__ alignas(16) uint8_t sc[kRows ? kAtoms * 512 : 16], sct[kCols ? kAtoms * 512 : 16];
@@ -89,8 +89,11 @@ __global__ void __launch_bounds__(kThreads, 3) quantize_kernel(const QuantParams
   for (int i = 0; i < kPasses; ++i) {
     const int r = (t >> 3) + i * kStep;
     if (kCols) {
-      *reinterpret_cast<uint4*>(tile + r * kPitch + c16 * 2) = va[i];
-      *reinterpret_cast<uint4*>(tile + r * kPitch + c16 * 2 + 16) = vb[i];
+      // (four lanes of a row begin with their second half: no two hit a bank)
+      uint8_t* o = tile + r * kPitch + c16 * 2;
+      const bool late = t & 4;
+      *reinterpret_cast<uint4*>(o + (late ? 16 : 0)) = late ? vb[i] : va[i];
+      *reinterpret_cast<uint4*>(o + (late ? 0 : 16)) = late ? va[i] : vb[i];
     }
     if (kRows) {
       float2 y[4], z[4];
@@ -128,15 +131,22 @@ __global__ void __launch_bounds__(kThreads, 3) quantize_kernel(const QuantParams
       const quant::GroupScale gb = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(mb), d);
       const bool in = m0 + grp * G < p.rows_padded;      // whole groups: rows_padded is a multiple of 32
 #pragma unroll
-      for (int w = 0; w < G / 8; ++w) {
-        float2 y[4];
-        uint8_t* o = ct + c * kCodePitch + grp * (G / 2) + w * 4;
+      for (int h = 0; h < 2; ++h) {
+        uint32_t q[G / 8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = make_float2(bf16_lo(v[w * 8 + 2 * e]), bf16_lo(v[w * 8 + 2 * e + 1]));
-        *reinterpret_cast<uint32_t*>(o) = quant::codes8<Codes::kE2M1, S>(y, ga).x;
+        for (int w = 0; w < G / 8; ++w) {
+          float2 y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = make_float2(bf16_hi(v[w * 8 + 2 * e]), bf16_hi(v[w * 8 + 2 * e + 1]));
-        *reinterpret_cast<uint32_t*>(o + kCodePitch) = quant::codes8<Codes::kE2M1, S>(y, gb).x;
+          for (int e = 0; e < 4; ++e)
+            y[e] = h ? make_float2(bf16_hi(v[w * 8 + 2 * e]), bf16_hi(v[w * 8 + 2 * e + 1]))
+                     : make_float2(bf16_lo(v[w * 8 + 2 * e]), bf16_lo(v[w * 8 + 2 * e + 1]));
+          q[w] = quant::codes8<Codes::kE2M1, S>(y, h ? gb : ga).x;
+        }
+        uint8_t* o = ct + (c + h) * kCodePitch;
+        if constexpr (G == 32)
+          *reinterpret_cast<uint4*>(o + ((grp ^ ((c >> 1) & 3)) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
+        else
+          *reinterpret_cast<uint2*>(o + (((grp >> 1) ^ ((c >> 1) & 3)) << 4) + (grp & 1) * 8) = make_uint2(q[0], q[1]);
       }
       uint8_t* o = sct + (grp >> 2) * 512 + (grp & 3);
       o[(c & 31) * 16 + (c >> 5) * 4] = static_cast<uint8_t>(in ? ga.byte : 0u);
@@ -150,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 3) quantize_kernel(const QuantParams
       const int ch = (t >> 2) + i * (kThreads / 4), part = t & 3;
       if (ch < nch && m0 + part * 32 < p.rows_padded)
         *reinterpret_cast<uint4*>(p.qt + (k0 + ch) * p.ld_qt + (m0 >> 1) + part * 16) =
-            *reinterpret_cast<const uint4*>(ct + ch * kCodePitch + part * 16);
+            *reinterpret_cast<const uint4*>(ct + ch * kCodePitch + ((part ^ ((ch >> 1) & 3)) << 4));
     }
   }
 }
