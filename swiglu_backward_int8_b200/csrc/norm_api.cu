@@ -59,10 +59,11 @@ int check_rows(const void* p, int64_t ld, int64_t channels) {
   return misaligned(p, 15) || (ld & 7) ? SDQ_ERR_ALIGN : SDQ_OK;
 }
 
-int launch(const void* kernel, dim3 grid, dim3 block, cudaStream_t stream, void** args) {
+int launch(const void* kernel, dim3 grid, dim3 block, cudaStream_t stream, void** args, size_t smem = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -224,19 +225,24 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
   p.weight_f32 = format & SDQ_FMT_WEIGHT_F32 ? 1 : 0;
   const int vecs = static_cast<int>((channels + 7) / 8);
   const int kv = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
-  const int threads = kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
+  int row_threads = kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
+  const int rows_cta = kv == 1 ? std::max(1, 256 / row_threads) : 1;
+  const int threads = row_threads * rows_cta;
   const int per_sm = kv ? std::min(4, ctas_per_sm(threads, sdq::norm::backward_regs(kv))) : 1;
-  p.parts = static_cast<int32_t>(std::min<int64_t>(rows, std::min<int64_t>(kMaxParts, int64_t{sms} * per_sm)));
-  void (*k)(BwdParams) = kv == 0   ? sdq::norm::rmsnorm_backward_long_kernel
-                         : kv == 1 ? sdq::norm::rmsnorm_backward_kernel<1>
-                         : kv == 2 ? sdq::norm::rmsnorm_backward_kernel<2>
-                                   : sdq::norm::rmsnorm_backward_kernel<4>;
-  void* args[] = {&p};
-  if (const int e = launch(reinterpret_cast<const void*>(k), dim3(p.parts), dim3(threads), s, args)) return e;
+  p.parts = static_cast<int32_t>(
+      std::min<int64_t>((rows + rows_cta - 1) / rows_cta, std::min<int64_t>(kMaxParts, int64_t{sms} * per_sm)));
+  const void* k = kv == 0   ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_long_kernel)
+                  : kv == 1 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<1>)
+                  : kv == 2 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<2>)
+                            : reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<4>);
+  // at most 256 / row_threads rows of 8 row_threads channels: 8 KB
+  const size_t smem = rows_cta > 1 ? static_cast<size_t>(rows_cta) * channels * 4 : 0;
+  void* args[] = {&p, &row_threads};
+  if (const int e = launch(k, dim3(p.parts), dim3(threads), s, args, smem)) return e;
   const float* part = p.part;
   void* args2[] = {&part, &p.gw, &p.parts, &p.channels};
   return launch(reinterpret_cast<const void*>(sdq::norm::grad_weight_kernel),
-                dim3(static_cast<unsigned>((channels + 31) / 32)), dim3(256), s, args2);
+                dim3(static_cast<unsigned>((channels + 31) / 32)), dim3(1024), s, args2);
 }
 
 }  // extern "C"

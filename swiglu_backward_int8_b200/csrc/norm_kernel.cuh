@@ -404,13 +404,21 @@ __device__ __forceinline__ float backward_factor(const BwdParams& p, float rstd,
 }
 
 // Rows that fit the registers, kVecs vectors a thread: grad_y and h of the next
-// row are loaded ahead, grad_h while the row's sum is added up.
+// row are loaded ahead, grad_h while the row's sum is added up.  Short rows go
+// several to a CTA (threads [0, row_threads) the first, and so on); its sums are
+// put together at the end, in the rows' order.
+// (kVecs above 1: one row, and the compiler knows.)
 template <int kVecs>
-__device__ __forceinline__ void rmsnorm_backward(const BwdParams& p) {
+__device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads) {
   __shared__ float red[2][32];
+  extern __shared__ float sums[];   // [rows of the CTA][channels], for several rows
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = threadIdx.x, threads = blockDim.x, warps = threads >> 5;
+  constexpr bool kSeveral = kVecs == 1;
+  const int row_threads = kSeveral ? threads : blockDim.x, row_warps = row_threads >> 5;
+  const int rows_cta = kSeveral ? blockDim.x / row_threads : 1;
+  const int t = kSeveral ? threadIdx.x % row_threads : threadIdx.x, mine = kSeveral ? threadIdx.x / row_threads : 0;
+  const int64_t stride = static_cast<int64_t>(p.parts) * rows_cta;
   float2 acc[kVecs][4] = {};
   uint4 gn[kVecs], hn[kVecs];
   auto load = [&](int64_t row) {
@@ -419,50 +427,60 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p) {
     const uint8_t* h = p.h + 2 * row * p.ld_h;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int k = (t + i * threads) * 8;
+      const int k = (t + i * row_threads) * 8;
       if (k < p.channels) {
         gn[i] = *reinterpret_cast<const uint4*>(gy + 2 * k);
         hn[i] = *reinterpret_cast<const uint4*>(h + 2 * k);
       }
     }
   };
-  load(blockIdx.x);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * rows_cta + mine;
+  load(row);
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
-    const float rstd = p.rstd[row];
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows_cta; base < p.rows; base += stride, row += stride) {
+    const bool on = !kSeveral || row < p.rows;
+    const float rstd = on ? p.rstd[row] : 0.0f;
     const uint8_t* gh = p.gh ? p.gh + 2 * row * p.ld_gh : nullptr;
     uint8_t* gx = p.gx + 2 * row * p.ld_gx;
     uint4 gv[kVecs], hv[kVecs], rv[kVecs];
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int k = (t + i * threads) * 8;
+      const int k = (t + i * row_threads) * 8;
       gv[i] = gn[i];
       hv[i] = hn[i];
       rv[i] = make_uint4(0, 0, 0, 0);
-      if (k < p.channels) {
+      if (on && k < p.channels) {
         if (gh) rv[i] = *reinterpret_cast<const uint4*>(gh + 2 * k);
         dot += dot8(p, k, gv[i], hv[i]);
       }
     }
-    load(row + p.parts);
-    dot = row_sum(dot, red[flip], warps);
+    load(row + stride);
+    dot = row_sum(dot, red[flip], row_warps);
     flip ^= 1;
     const float c = backward_factor(p, rstd, dot);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int k = (t + i * threads) * 8;
-      if (k < p.channels) backward8(p, gx, k, gv[i], hv[i], rv[i], rstd, c, acc[i]);
+      const int k = (t + i * row_threads) * 8;
+      if (on && k < p.channels) backward8(p, gx, k, gv[i], hv[i], rv[i], rstd, c, acc[i]);
     }
   }
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int k = (t + i * threads) * 8;
+    const int k = (t + i * row_threads) * 8;
     if (k < p.channels) {
-      float4* q = reinterpret_cast<float4*>(part + k);
+      float4* q = reinterpret_cast<float4*>((rows_cta > 1 ? sums + mine * p.channels : part) + k);
       q[0] = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
       q[1] = make_float4(acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y);
+    }
+  }
+  if (rows_cta > 1) {
+    __syncthreads();
+    for (int k = threadIdx.x; k < p.channels; k += blockDim.x) {
+      float s = sums[k];
+      for (int r = 1; r < rows_cta; ++r) s += sums[r * p.channels + k];
+      part[k] = s;
     }
   }
 }
@@ -471,8 +489,8 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p) {
 constexpr int backward_regs(int vecs) { return vecs == 1 ? 64 : vecs == 2 ? 80 : 128; }
 
 template <int kVecs>
-__global__ void __maxnreg__(backward_regs(kVecs)) rmsnorm_backward_kernel(const BwdParams p) {
-  rmsnorm_backward<kVecs>(p);
+__global__ void __maxnreg__(backward_regs(kVecs)) rmsnorm_backward_kernel(const BwdParams p, int row_threads) {
+  rmsnorm_backward<kVecs>(p, row_threads);
 }
 
 // Longer rows: read twice, the sums of grad_y n in memory between rows (a
@@ -513,24 +531,25 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_long_kernel(cons
   }
 }
 
-// gw[k] = sum over the rows of part: 32 columns a CTA, a warp takes every
-// eighth row, then the eight sums are added in order.
-__global__ void __launch_bounds__(256) grad_weight_kernel(const float* part, float* gw, int32_t parts, int32_t channels) {
-  __shared__ float sum[8][32];
+// gw[k] = sum over the rows of part: 32 columns a CTA, a warp takes every 32nd
+// row, then the 32 sums are added as a tree.
+__global__ void __launch_bounds__(1024) grad_weight_kernel(const float* part, float* gw, int32_t parts, int32_t channels) {
+  __shared__ float sum[32][33];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  if (k < channels)
-    for (int r = warp; r < parts; r += 8) s += part[static_cast<int64_t>(r) * channels + k];
+  if (k < channels) {
+#pragma unroll 4
+    for (int r = warp; r < parts; r += 32) s += part[static_cast<int64_t>(r) * channels + k];
+  }
   sum[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && k < channels) {
+  s = sum[lane][warp];   // column `warp`, the sum of warp `lane`
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sum[i][lane];
-    gw[k] = s;
-  }
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane == 0 && blockIdx.x * 32 + warp < channels) gw[blockIdx.x * 32 + warp] = s;
 }
 
 }  // namespace norm
