@@ -304,3 +304,10 @@ def sdq_rmsnorm_backward_workspace_bytes(rows: int, channels: int) -> int:
 
 def sdq_fp4_scale_bytes(rows: int, k: int, format: int) -> int:
     return int(_lib.sdq_fp4_scale_bytes(rows, k, format))
+
+
+def entry_addresses() -> tuple:
+    """Addresses of the entries that the extension module calls, in its order."""
+    return tuple(ctypes.cast(getattr(_lib, f), _P).value
+                 for f in ("sdq_rmsnorm_quant", "sdq_rmsnorm_backward", "sdq_rmsnorm_backward_workspace_bytes",
+                           "sdq_quantize_fp4", "sdq_dequantize_fp4", "sdq_matmul_fp4"))

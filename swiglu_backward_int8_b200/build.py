@@ -10,7 +10,9 @@ nvcc compiles ``csrc/sdq_api.cu`` (host API + the fused kernel),
 4-bit quantizer and product), each in a process of its own, and links them into
 a shared library with a C ABI (``include/sdq.h``); the CUDA runtime is linked
 statically and the driver's tensor-map encoder is looked up at run time, so
-the library needs only the NVIDIA driver at load time.
+the library needs only the NVIDIA driver at load time.  ``csrc/marshal.cpp``, the
+short way from torch tensors to the library's entries, becomes the extension
+module ``_marshal.so`` against the installed torch.
 """
 from __future__ import annotations
 
@@ -26,6 +28,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsdq.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 OBJECTS = os.path.join(PKG, "_build")   # one object a source, kept for the next build
 SOURCES = [os.path.join(CSRC, f) for f in ("sdq_api.cu", "fwd_api.cu", "norm_api.cu", "fp4_api.cu")]
 DEPS = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)) + [os.path.join(INCLUDE, "sdq.h")]
@@ -74,16 +78,35 @@ def _compile(source: str, obj: str, force: bool, verbose: bool) -> None:
     os.replace(tmp, obj)
 
 
+def _compile_marshal(verbose: bool) -> None:
+    """The extension module: the host compiler, torch's headers and libraries."""
+    import sysconfig
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    includes = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(base, "lib")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(f"-I{i}" for i in includes), MARSHAL_SOURCE, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+          "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"], verbose)
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libsdq.so if it is missing or older than its sources."""
-    if (not force and os.path.exists(LIB)
-            and os.path.getmtime(LIB) >= max(os.path.getmtime(f) for f in DEPS)):
+    """Compile libsdq.so and _marshal.so if one is missing or older than the sources."""
+    if not force and all(os.path.exists(so) and os.path.getmtime(so) >= max(os.path.getmtime(f) for f in DEPS)
+                         for so in (LIB, MARSHAL)):
         return LIB
     os.makedirs(OBJECTS, exist_ok=True)
     objects = [os.path.join(OBJECTS, os.path.basename(s) + ".o") for s in SOURCES]
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as pool:
+        marshal = pool.submit(_compile_marshal, verbose)
         for _ in pool.map(lambda so: _compile(*so, force, verbose), zip(SOURCES, objects)):
             pass
+        marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     _run([nvcc(), *ARCH, "-shared", *objects, "-o", tmp], verbose)
     os.replace(tmp, LIB)

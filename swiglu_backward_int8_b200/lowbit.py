@@ -19,10 +19,16 @@ from typing import Optional, Tuple
 
 import torch
 
+from . import _marshal
 from ._check import _rows
 from ._lib import (FMT_E2M1, FMT_E4M3, FMT_E8M0, FMT_OUT_F32, FMT_SCALE_E4M3, FMT_WEIGHT_F32,
-                   sdq_dequantize_fp4, sdq_matmul_fp4, sdq_quantize_fp4, sdq_rmsnorm_backward,
+                   SdqError, entry_addresses, sdq_dequantize_fp4, sdq_matmul_fp4, sdq_quantize_fp4, sdq_rmsnorm_backward,
                    sdq_rmsnorm_backward_workspace_bytes, sdq_rmsnorm_quant)
+
+# Each function below first offers its arguments to its namesake in csrc/marshal.cpp,
+# which makes the ordinary call (every output given, on the current device) and
+# answers with its status, or with -1: then the checks and allocations here run.
+_marshal.bind(*entry_addresses())
 
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
@@ -35,6 +41,13 @@ _SCALES_OF = {torch.float32: "fp32", torch.float8_e8m0fnu: "e8m0", torch.uint8: 
               torch.float8_e4m3fn: "e4m3"}
 _FP4_GROUP = {"e8m0": 32, "e4m3": 16}
 _FP4_FORMAT = {"e8m0": FMT_E8M0, "e4m3": FMT_SCALE_E4M3}
+
+
+def _made(status: int, entry: str) -> bool:
+    """Whether the short way made the call."""
+    if status > 0:
+        raise SdqError(status, entry)
+    return status == 0
 
 
 def fp4_scale_shape(rows: int, k: int, scales: str = "e8m0") -> Tuple[int, int, int]:
@@ -67,21 +80,8 @@ def _tiles(name: str, s: torch.Tensor, rows: int, k: int, scales: str, device) -
     return s.data_ptr()
 
 
-def _ld(name: str, t: torch.Tensor, rows: int, cols: int, dtypes, device) -> int:
-    """The leading dimension of a 2-D row-major operand.  A small call spends
-    most of its time in such checks: what is in order passes here, the rest goes
-    to the check that says what is wrong."""
-    if t.dtype in dtypes and t.shape == (rows, cols) and t.get_device() == device.index:
-        ld, unit = t.stride()
-        if unit == 1 and ld >= cols and rows > 1:
-            return ld
-        if unit == 1 and rows == 1:
-            return cols
-    return _rows(name, t, (rows, cols), dtypes, True, device)
-
-
 def _codes(name: str, q: torch.Tensor, rows: int, k: int, device) -> int:
-    return _ld(name, q, rows, k // 2, _U8, device)
+    return _rows(name, q, (rows, k // 2), _U8, True, device)
 
 
 def _length(k: int) -> None:
@@ -117,20 +117,8 @@ def _two_d(name: str, t: torch.Tensor) -> Tuple[int, int]:
 
 def _call(entry, device, *args) -> None:
     """The entry point on the device's current stream."""
-    index = device.index
-    if torch.cuda.current_device() == index:
-        entry(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(device):
-            entry(*args, _raw_stream(index))
-
-
-def _stream_of(index: int) -> int:
-    return torch.cuda.current_stream(index).cuda_stream
-
-
-# (the stream's address without a Stream object around it, 2 us cheaper)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+    with torch.cuda.device(device):
+        entry(*args, torch.cuda.current_stream(device).cuda_stream)
 
 
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -154,6 +142,9 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
     ``h`` may be x or residual itself.  Optional outputs: ``y`` (bf16, the
     normed rows) and ``rstd`` (fp32 [rows], for ``rmsnorm_backward``).
     ``global_scale``: the scale per tensor of "e2m1" codes with "e4m3" scales."""
+    if _made(_marshal.rmsnorm_quant(x, weight, residual, eps, group_size, codes, scales, q, s, h, y, rstd, global_scale),
+             "sdq_rmsnorm_quant"):
+        return q, s, (x if residual is None else h)
     rows, channels = _two_d("x", x)
     dev = x.device
     codes = codes or ("int8" if q is None else _CODES_OF.get(q.dtype))
@@ -172,14 +163,14 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
     fmt = {"int8": 0, "e4m3": FMT_E4M3, "e2m1": FMT_E2M1}[codes] | \
         {"fp32": 0, "e8m0": FMT_E8M0, "e4m3": FMT_SCALE_E4M3}[scales] | \
         (FMT_WEIGHT_F32 if weight.dtype == torch.float32 else 0)
-    ld_x = _ld("x", x, rows, channels, _BF16, dev)
+    ld_x = _rows("x", x, (rows, channels), _BF16, True, dev)
     wp = _vector("weight", weight, channels, _WEIGHT, dev)
     rp, ld_r, hp, ld_h = None, 0, None, 0
     if residual is not None:
-        rp, ld_r = residual.data_ptr(), _ld("residual", residual, rows, channels, _BF16, dev)
+        rp, ld_r = residual.data_ptr(), _rows("residual", residual, (rows, channels), _BF16, True, dev)
         if h is None:
             h = torch.empty((rows, channels), dtype=torch.bfloat16, device=dev)
-        hp, ld_h = h.data_ptr(), _ld("h", h, rows, channels, _BF16, dev)
+        hp, ld_h = h.data_ptr(), _rows("h", h, (rows, channels), _BF16, True, dev)
     elif h is not None:
         raise ValueError("h is written only with a residual")
     else:
@@ -197,11 +188,11 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
             q = torch.empty((rows, channels), dtype=_CODES[codes], device=dev)
         if s is None:
             s = torch.empty((rows, groups), dtype=_SCALES[scales], device=dev)
-        ld_q = _ld("q", q, rows, channels, (_CODES[codes],), dev)
-        ld_s = _ld("s", s, rows, groups, (s.dtype,), dev)
+        ld_q = _rows("q", q, (rows, channels), (_CODES[codes],), True, dev)
+        ld_s = _rows("s", s, (rows, groups), (s.dtype,), True, dev)
     yp, ld_y = None, 0
     if y is not None:
-        yp, ld_y = y.data_ptr(), _ld("y", y, rows, channels, _BF16, dev)
+        yp, ld_y = y.data_ptr(), _rows("y", y, (rows, channels), _BF16, True, dev)
     _call(sdq_rmsnorm_quant, dev, x.data_ptr(), ld_x, rp, ld_r, wp, hp, ld_h, q.data_ptr(), ld_q, s.data_ptr(), ld_s,
           yp, ld_y, None if rstd is None else _vector("rstd", rstd, rows, _F32, dev),
           _one("global_scale", global_scale, scales, dev), rows, channels, group_size, fmt, eps)
@@ -219,18 +210,21 @@ def rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     grad_y, h or grad_h itself.  ``workspace``: uint8, at least
     ``sdq_rmsnorm_backward_workspace_bytes(rows, channels)`` bytes (allocated where
     not given); calls that overlap need one each."""
+    if _made(_marshal.rmsnorm_backward(grad_y, h, weight, rstd, grad_h, grad_x, grad_weight, workspace),
+             "sdq_rmsnorm_backward"):
+        return grad_x, grad_weight
     rows, channels = _two_d("grad_y", grad_y)
     dev = grad_y.device
     need = sdq_rmsnorm_backward_workspace_bytes(rows, channels)
     if need == 0:
         raise ValueError(f"{channels} channels: a positive multiple of 16 is needed")
-    ld_gy = _ld("grad_y", grad_y, rows, channels, _BF16, dev)
-    ld_h = _ld("h", h, rows, channels, _BF16, dev)
+    ld_gy = _rows("grad_y", grad_y, (rows, channels), _BF16, True, dev)
+    ld_h = _rows("h", h, (rows, channels), _BF16, True, dev)
     wp = _vector("weight", weight, channels, _WEIGHT, dev)
     sp = _vector("rstd", rstd, rows, _F32, dev)
     ghp, ld_gh = None, 0
     if grad_h is not None:
-        ghp, ld_gh = grad_h.data_ptr(), _ld("grad_h", grad_h, rows, channels, _BF16, dev)
+        ghp, ld_gh = grad_h.data_ptr(), _rows("grad_h", grad_h, (rows, channels), _BF16, True, dev)
     if grad_x is None:
         grad_x = torch.empty((rows, channels), dtype=torch.bfloat16, device=dev)
     if grad_weight is None:
@@ -240,7 +234,7 @@ def rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
     _call(sdq_rmsnorm_backward, dev, grad_y.data_ptr(), ld_gy, h.data_ptr(), ld_h, wp, sp, ghp, ld_gh,
-          grad_x.data_ptr(), _ld("grad_x", grad_x, rows, channels, _BF16, dev),
+          grad_x.data_ptr(), _rows("grad_x", grad_x, (rows, channels), _BF16, True, dev),
           _vector("grad_weight", grad_weight, channels, _F32, dev), rows, channels,
           FMT_WEIGHT_F32 if weight.dtype == torch.float32 else 0, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
@@ -258,13 +252,15 @@ def quantize_fp4(x: torch.Tensor, scales: Optional[str] = None, axis: str = "row
     multiple of 32; the missing ones count as zeros.  What is not given is
     allocated; ``scales`` ("e8m0", the default, or "e4m3") follows the given
     tiles."""
+    if _made(_marshal.quantize_fp4(x, scales, axis, q, s, q_t, s_t, global_scale), "sdq_quantize_fp4"):
+        return (q, s) if axis == "rows" else (q_t, s_t) if axis == "columns" else (q, s, q_t, s_t)
     rows, channels = _two_d("x", x)
     dev = x.device
     if axis not in ("rows", "columns", "both"):
         raise ValueError(f"axis is \"rows\", \"columns\" or \"both\", not {axis!r}")
     scales = _scales_of(s if s is not None else s_t, scales, "e8m0")
     fp4_scale_shape(rows, channels, scales)   # channels a multiple of 32, 4-bit scales
-    ld_x = _ld("x", x, rows, channels, _BF16, dev)
+    ld_x = _rows("x", x, (rows, channels), _BF16, True, dev)
     padded = -(-rows // 32) * 32
     out: list = []
     args: list = []
@@ -293,6 +289,8 @@ def quantize_fp4(x: torch.Tensor, scales: Optional[str] = None, axis: str = "row
 def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, global_scale: Optional[torch.Tensor] = None, *,
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of 4-bit codes and scale tiles, bf16 [rows, k]."""
+    if _made(_marshal.dequantize_fp4(q, s, global_scale, out), "sdq_dequantize_fp4"):
+        return out
     rows, k = _two_d("q", q)
     k *= 2
     dev = q.device
@@ -302,7 +300,7 @@ def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, global_scale: Optional[torc
     if out is None:
         out = torch.empty((rows, k), dtype=torch.bfloat16, device=dev)
     _call(sdq_dequantize_fp4, dev, q.data_ptr(), ld_q, sp, _one("global_scale", global_scale, scales, dev),
-          out.data_ptr(), _ld("out", out, rows, k, _BF16, dev), rows, k, _FP4_FORMAT[scales])
+          out.data_ptr(), _rows("out", out, (rows, k), _BF16, True, dev), rows, k, _FP4_FORMAT[scales])
     return out
 
 
@@ -312,6 +310,8 @@ def matmul_fp4(a: torch.Tensor, a_s: torch.Tensor, b: torch.Tensor, b_s: torch.T
     """The product of two 4-bit operands, out[i, j] = sum_k a[i, k] b[j, k],
     summed in fp32: a [m, k] and b [n, k] as codes and scale tiles of one format,
     out [m, n] bf16 (the default) or float32."""
+    if _made(_marshal.matmul_fp4(a, a_s, b, b_s, a_global, b_global, out, out_dtype), "sdq_matmul_fp4"):
+        return out
     m, ka = _two_d("a", a)
     n, kb = _two_d("b", b)
     if ka != kb:
@@ -325,7 +325,7 @@ def matmul_fp4(a: torch.Tensor, a_s: torch.Tensor, b: torch.Tensor, b_s: torch.T
         out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")
-    ld_out = _ld("out", out, m, n, _WEIGHT, dev)
+    ld_out = _rows("out", out, (m, n), _WEIGHT, True, dev)
     _call(sdq_matmul_fp4, dev, a.data_ptr(), ld_a, ap, _one("a_global", a_global, scales, dev), b.data_ptr(), ld_b, bp,
           _one("b_global", b_global, scales, dev), out.data_ptr(), ld_out, m, n, k,
           _FP4_FORMAT[scales] | (FMT_OUT_F32 if out.dtype == torch.float32 else 0))
