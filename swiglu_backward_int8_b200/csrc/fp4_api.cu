@@ -128,7 +128,7 @@ int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
   return launch(kern.fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kPairThreads, kern.smem, c.stream, args);
 }
 
-// Few rows of a: clusters that share the steps along k.
+// Few rows of a, or few tiles: clusters that share the steps along k.
 template <Scales S>
 int launch_strip(const Product& c, int sms) {
   using Z = sdq::mm4::StripShape<S>;
@@ -157,9 +157,17 @@ int launch_strip(const Product& c, int sms) {
   if (const int e = limit.set(fn, 210 * 1024)) return e;
   const int64_t tiles = p.tiles_b * ((c.m + p.cols - 1) / p.cols);
   const int64_t steps = (c.k + sdq::mm4::kStepCodes - 1) / sdq::mm4::kStepCodes;
+  // CTAs that share the steps along k: as many as the device holds, while the
+  // steps saved outweigh the exchange of the sums.  Up to 32 columns that takes
+  // 1.5 us and a step 0.3 (1 x 4096 x 7168: 11.2, 8.2, 7.0, 7.0 us with 1, 2, 4,
+  // 8 CTAs); with more columns it grows (61 x 7168 x 4096, 16 steps: 9.0 us with
+  // one CTA and with two, 15.9 with four).
+  const bool narrow = p.cols <= sdq::mm4::kNarrow;
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= (p.cols <= 32 ? 2 : 1) * sms && steps >= 4 * split) split *= 2;
+  while (split < 8 && tiles * split * 2 <= (narrow ? 2 : 1) * sms && steps >= (narrow ? 4 : 24) * split) split *= 2;
   p.stages = Z::stages(p.cols, split);
+  p.share = Z::share(p.cols, split);
+  for (int s = p.share; s > 1; s /= 2) ++p.share_log;
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage + Z::sums(p.cols, split);
   void* args[] = {&mb, &ma, &p};
   return launch(fn, static_cast<unsigned>(tiles * split), sdq::mm4::kThreads, smem, c.stream, args, split);
@@ -280,7 +288,10 @@ int sdq_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_
   if (const int e = sdq_internal::sm_count(&sms)) return e;
   const Product c = {a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format, static_cast<cudaStream_t>(stream)};
   const bool e8m0 = format & SDQ_FMT_E8M0, f32 = format & SDQ_FMT_OUT_F32;
-  if (m <= 128) return e8m0 ? launch_strip<Scales::kE8M0>(c, sms) : launch_strip<Scales::kE4M3>(c, sms);
+  // Tiles of 128 x 128 that the device takes at once: 128 columns a CTA keep more
+  // multiprocessors busy than 256 x 256 outputs a pair (256 x 1024 x 1024: 5.1 us
+  // instead of 5.7; 1024 x 1024 x 4096: 9.4 instead of 9.8).
+  if (m <= 128 || (m + 127) / 128 * ((n + 127) / 128) <= sms) return e8m0 ? launch_strip<Scales::kE8M0>(c, sms) : launch_strip<Scales::kE4M3>(c, sms);
   return launch_pair(c, e8m0 ? pair_of<Scales::kE8M0, 256>(f32) : pair_of<Scales::kE4M3, 256>(f32), sms);
 }
 

@@ -43,6 +43,7 @@ struct Params {
   int32_t cols;            // columns a CTA computes: a multiple of 16, at most 128
   int32_t tiles_b;         // blocks of 128 rows of B
   int32_t stages, stage;   // the shared-memory ring
+  int32_t share, share_log;   // columns that belong to a CTA of a cluster: a power of two
   int32_t out_f32;         // fp32 elements instead of bf16
   int* status;
   uint64_t wait_limit_ns;
@@ -207,12 +208,13 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void store_cluster4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
 }
-__device__ __forceinline__ float load_shared(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 load_shared4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
@@ -222,21 +224,30 @@ __device__ __forceinline__ float load_shared(uint32_t addr) {
 // columns, so an instruction is no wider than A needs.  The CTAs of a cluster take
 // the steps along k in turn, so that there are about as many CTAs as the device
 // holds; each sends its sums to the CTA that a column belongs to (column c to rank
-// c mod the cluster's size), which adds them up in the order of the ranks: the
-// result does not depend on timing.  (Sending takes one barrier of the cluster;
-// reading the others' sums took two, and a latency a number.)  Up to 32 columns
-// two CTAs fit a multiprocessor: a kernel's set-up is under way while the one
-// before it still runs.
+// c / share), which adds them up in the order of the ranks: the result does not
+// depend on timing.  (Sending takes one barrier of the cluster; reading the
+// others' sums took two, and a latency a number.)  Up to 32 columns two CTAs fit a
+// multiprocessor: a kernel's set-up is under way while the one before it still
+// runs.
 
-__device__ __forceinline__ void store_out(const Params& p, int64_t row, int64_t col, float v) {
-  const int64_t at = row * p.ld_out + col;
-  if (p.out_f32)
-    reinterpret_cast<float*>(p.out)[at] = v;
-  else
-    reinterpret_cast<uint16_t*>(p.out)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
-}
+// Where a lane's next output goes: its column of `out`, a row further each time.
+struct Column {
+  uint8_t* at;
+  int64_t step;
+  int f32;
+  __device__ __forceinline__ Column(const Params& p, int64_t row, int64_t col)
+      : at(p.out + (row * p.ld_out + col) * (p.out_f32 ? 4 : 2)), step(p.ld_out * (p.out_f32 ? 4 : 2)), f32(p.out_f32) {}
+  __device__ __forceinline__ void put(float v) {
+    if (f32)
+      *reinterpret_cast<float*>(at) = v;
+    else
+      *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+    at += step;
+  }
+};
 
 constexpr int kMaxStages = 8;
+constexpr int kNarrow = 32;   // columns up to which two CTAs share a multiprocessor
 
 template <Scales S>
 struct StripShape {
@@ -247,9 +258,15 @@ struct StripShape {
   static constexpr int kCols = 256;                                // 128 sums and two sets of scales used in turn
   static_assert(128 + 2 * kColsScale <= kCols, "the sums and the scales fit");
   static int stage(int cols) { return kCodesB + cols * kStepBytes + 2 * kScale; }   // a multiple of 1024
-  static int sums(int cols, int split) { return split > 1 ? (cols + split - 1) / split * split * kRows * 4 : 0; }
+  // Columns that belong to a CTA: a power of two, at least the four of a vector.
+  static int share(int cols, int split) {
+    int s = 4;
+    while (s * split < cols) s *= 2;
+    return s;
+  }
+  static int sums(int cols, int split) { return split > 1 ? split * share(cols, split) * kRows * 4 : 0; }
   static int stages(int cols, int split) {
-    const int n = ((cols <= 32 ? 108 : 208) * 1024 - sums(cols, split)) / stage(cols);
+    const int n = ((cols <= kNarrow ? 108 : 208) * 1024 - sums(cols, split)) / stage(cols);
     return n > kMaxStages ? kMaxStages : n;
   }
 };
@@ -295,7 +312,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = *const_cast<volatile uint32_t*>(&tmem_addr);
   const Sync sync = {p.status, &abort_flag, p.wait_limit_ns};
   const uint32_t parts = ring + p.stages * p.stage;   // the sums that this CTA receives
-  const int share = (p.cols + ranks - 1) / ranks;     // columns that belong to a CTA
+  // The sums of a rank's row lie in vectors of four, swizzled by the row so that
+  // neither the senders' lanes nor the reader's meet in a bank.
+  const int vecs = p.share >> 2, mask = vecs < 8 ? vecs - 1 : 7, shift = vecs < 2 ? 3 : vecs < 4 ? 2 : vecs < 8 ? 1 : 0;
+  auto slot = [&](int from, int row, int vec) {
+    return parts + static_cast<uint32_t>(((from * kRows + row) * vecs + (vec ^ ((row >> shift) & mask))) << 4);
+  };
 
   if (warp == 0) {
     if (elect_one()) {
@@ -354,20 +376,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       cluster_wait();
     }
+    Column mine(p, a0, b0 + row);
     for (int c = 0; ok && c < cols; c += 16) {
       uint32_t r[16];
       load_sums16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, r);
       load_wait();
       if (ranks > 1) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int owner = (c + e) % ranks, j = (c + e) / ranks;
-          store_cluster(at_rank(parts + ((rank * share + j) * kRows + row) * 4, owner), r[e]);
-        }
+        for (int e = 0; e < 16; e += 4)
+          store_cluster4(at_rank(slot(rank, row, ((c + e) & (p.share - 1)) >> 2), (c + e) >> p.share_log), &r[e]);
       } else if (b0 + row < p.rows_b) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (c + e < cols) store_out(p, a0 + c + e, b0 + row, __uint_as_float(r[e]) * alpha);
+          if (c + e < cols) mine.put(__uint_as_float(r[e]) * alpha);
       }
     }
     fence_before();
@@ -376,12 +397,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       cluster_arrive();
       cluster_wait();
       if (b0 + row < p.rows_b) {
-        for (int j = 0; j * ranks + rank < cols; ++j) {
-          float v = load_shared(parts + (j * kRows + row) * 4);
+        const int first = rank * p.share, last = min(first + p.share, cols);
+        Column out(p, a0 + first, b0 + row);
+        for (int c = first; c < last; c += 4) {
+          float4 v = load_shared4(slot(0, row, (c - first) >> 2));
 #pragma unroll
-          for (int r = 1; r < 8; ++r)
-            if (r < ranks) v += load_shared(parts + ((r * share + j) * kRows + row) * 4);
-          store_out(p, a0 + j * ranks + rank, b0 + row, v * alpha);
+          for (int r = 1; r < 8; ++r) {
+            if (r < ranks) {
+              const float4 u = load_shared4(slot(r, row, (c - first) >> 2));
+              v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+          }
+          const float s[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < last) out.put(s[e] * alpha);
         }
       }
     }

@@ -151,13 +151,10 @@ int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t
   p.weight_f32 = format & SDQ_FMT_WEIGHT_F32 ? 1 : 0;
   p.eps = eps;
   const int vecs = static_cast<int>(channels / sdq::norm::kVec);
-  // Few rows: a vector a thread, latency counts.  Many: two, and the next row
-  // loaded ahead.  Rows that neither holds: read again.
-  const Variant v = rows <= sms && vecs <= sdq::norm::kMaxThreads               ? Variant::kFew
-                    : vecs <= sdq::norm::kAheadThreads * sdq::norm::kAheadVecs ? Variant::kMany
-                                                                               : Variant::kLong;
-  const int each = v == Variant::kMany ? sdq::norm::kAheadVecs : 1;
-  int row_threads = v == Variant::kLong ? sdq::norm::kMaxThreads : round_up((vecs + each - 1) / each, 32);
+  // A vector a thread.  Few rows: each its own CTA.  Many: a persistent grid,
+  // the next row loaded ahead.  Rows that no CTA holds: read again.
+  const Variant v = vecs > sdq::norm::kMaxThreads ? Variant::kLong : rows <= sms ? Variant::kFew : Variant::kMany;
+  int row_threads = v == Variant::kLong ? sdq::norm::kMaxThreads : round_up(vecs, 32);
   const int rows_cta = v == Variant::kMany ? std::max(1, 128 / row_threads) : 1;
   int64_t grid = (rows + rows_cta - 1) / rows_cta;
   if (v == Variant::kMany)

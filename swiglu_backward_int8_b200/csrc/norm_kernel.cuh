@@ -168,33 +168,27 @@ __device__ __forceinline__ void store_scale(const Params& p, int64_t row, int32_
 }
 
 // Threads [0, row_threads) of a CTA take its first row, and so on.  A thread
-// holds vectors of 16 consecutive channels, the next thread the next 16, so a
+// holds a vector of 16 consecutive channels, the next thread the next 16, so a
 // group of 16 to 256 channels is 1 to 16 neighbouring lanes of a warp.
 
-// The codes and scales of vector k of a row whose rstd is known.  rg: the scale
-// of the whole row (group 0), else set here.
+// The largest magnitude of a group from that of each lane's vector.
 template <Codes C, Scales S>
-__device__ __forceinline__ void finish(const Params& p, int64_t row, int32_t k, bool act, int t, const Vec& h, float rstd,
-                                       const quant::Divisor& d, quant::GroupScale& rg) {
-  Pairs y = {};
-  uint32_t m = 0;
-  if (act) m = norm_vec(p, h, k, rstd, y);
-  if (C == Codes::kE2M1 || p.group != 0) {
-    int lanes = 1;   // of a group
-    if (C != Codes::kE2M1 || S == Scales::kE8M0) {   // 32 channels at least
-      lanes = 2;
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    }
-    if (C != Codes::kE2M1) {
-      lanes = p.group >> 4;
-      if (lanes > 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      if (lanes > 4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
-      if (lanes > 8) m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
-    }
-    rg = quant::group_scale<C, S>(m, d);
-    if (act && (t & (lanes - 1)) == 0) store_scale<C, S>(p, row, (k >> 4) / lanes, rg);
+__device__ __forceinline__ uint32_t group_max(int32_t group, uint32_t m) {
+  if (C != Codes::kE2M1 || S == Scales::kE8M0) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));   // 32 channels at least
+  if (C != Codes::kE2M1) {
+    if (group > 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (group > 64) m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    if (group > 128) m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
   }
-  if (act) store_codes<C, S>(p, row, k, y, rg);
+  return m;
+}
+
+// The group of channel k, where k begins it; -1 elsewhere.
+template <Codes C, Scales S>
+__device__ __forceinline__ int32_t group_begun(int32_t group, int32_t k) {
+  if (C == Codes::kE2M1) return S == Scales::kE4M3 ? k >> 4 : (k & 31) ? -1 : k >> 5;
+  const int shift = 31 - __clz(group);   // a power of two
+  return (k & (group - 1)) ? -1 : k >> shift;
 }
 
 __device__ __forceinline__ float rstd_of(const Params& p, float ss) {
@@ -208,91 +202,73 @@ __device__ __forceinline__ void pad_scales(const Params& p, int64_t row, int t) 
   if (C == Codes::kE2M1 && t < p.tiles_k * 4 - p.groups) p.s[quant::tiled_scale(row, p.groups + t, p.tiles_k)] = 0;
 }
 
-// Rows that fit the registers, kVecs vectors a thread.  With kAhead a
-// persistent grid, the loads of the next row under way while a row is
-// reduced, normed and stored: else a multiprocessor's loads come in bursts
-// with pauses between them.
-template <Codes C, Scales S, int kVecs, bool kAhead>
+// Rows that fit a CTA, a vector a thread.  With kAhead a persistent grid, the
+// loads of the next row under way while a row is reduced, normed and stored:
+// else a multiprocessor's loads come in bursts with pauses between them.
+template <Codes C, Scales S, bool kAhead>
 __device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) {
   __shared__ float red[2][2][32];
   grid_dependency_wait();   // inputs may come from the previous kernel in the stream
   grid_launch_dependents();
   const int row_warps = row_threads >> 5, rows_cta = blockDim.x / row_threads;
-  const int t = threadIdx.x % row_threads;
+  const int t = threadIdx.x % row_threads, k = t * kVec;
+  const bool in = k < p.channels;
   const quant::Divisor d = quant::divisor<C, S>(p.global);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
   int64_t row = static_cast<int64_t>(blockIdx.x) * rows_cta + threadIdx.x / row_threads;
-  Vec x[kVecs], r[kVecs];
+  Vec x = {}, r = {};
   auto load = [&](int64_t from) {
-    if (from >= p.rows) return;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int k = (t + i * row_threads) * kVec;
-      if (k < p.channels) {
-        x[i] = load_vec(p.x + 2 * from * p.ld_x, k);
-        if (p.residual) r[i] = load_vec(p.residual + 2 * from * p.ld_residual, k);
-      }
-    }
+    if (from >= p.rows || !in) return;
+    x = load_vec(p.x + 2 * from * p.ld_x, k);
+    if (p.residual) r = load_vec(p.residual + 2 * from * p.ld_residual, k);
   };
   load(row);
   int flip = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows_cta; base < p.rows; base += stride, row += stride) {
-    const bool on = row < p.rows;
-    Vec h[kVecs];
+    const bool on = in && row < p.rows;
+    Vec h = {};
     float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int k = (t + i * row_threads) * kVec;
-      h[i] = {};
-      if (on && k < p.channels) {
-        h[i] = x[i];
-        if (p.residual) {
-          h[i] = {add_bf16x8(x[i].a, r[i].a), add_bf16x8(x[i].b, r[i].b)};
-          store_vec(p.h + 2 * row * p.ld_h, k, h[i]);
-        }
-        ss += sumsq(h[i]);
+    if (on) {
+      h = x;
+      if (p.residual) {
+        h = {add_bf16x8(x.a, r.a), add_bf16x8(x.b, r.b)};
+        store_vec(p.h + 2 * row * p.ld_h, k, h);
       }
+      ss = sumsq(h);
     }
     if (kAhead) load(row + stride);
     ss = row_sum(ss, red[flip][0], row_warps);
     const float rstd = rstd_of(p, ss);
     if (on && t == 0 && p.rstd) p.rstd[row] = rstd;
-    quant::GroupScale rg;
-    if (C != Codes::kE2M1 && p.group == 0) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int k = (t + i * row_threads) * kVec;
-        Pairs y;
-        if (on && k < p.channels) m = max(m, norm_vec(p, h[i], k, rstd, y));
-      }
-      rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[flip][1]), row_warps), d);
-      if (on && t == 0) store_scale<C, S>(p, row, 0, rg);
-    }
+    Pairs y = {};
+    uint32_t m = on ? norm_vec(p, h, k, rstd, y) : 0;
+    const bool whole = C != Codes::kE2M1 && p.group == 0;   // one scale a row
+    m = whole ? row_max(m, reinterpret_cast<uint32_t*>(red[flip][1]), row_warps) : group_max<C, S>(p.group, m);
     flip ^= 1;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int k = (t + i * row_threads) * kVec;
-      finish<C, S>(p, row, k, on && k < p.channels, t, h[i], rstd, d, rg);
+    const quant::GroupScale g = quant::group_scale<C, S>(m, d);
+    if (on) {
+      const int32_t begun = whole ? (t == 0 ? 0 : -1) : group_begun<C, S>(p.group, k);
+      if (begun >= 0) store_scale<C, S>(p, row, begun, g);
+      store_codes<C, S>(p, row, k, y, g);
     }
-    if (on) pad_scales<C>(p, row, t);
+    if (row < p.rows) pad_scales<C>(p, row, t);   // (a short row has fewer vectors than groups to pad)
     if (!kAhead) break;   // one row a thread
   }
 }
 
-// Few rows: one vector a thread.
+// Few rows: each has a CTA.
 template <Codes C, Scales S>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(const Params p, int row_threads) {
-  rmsnorm_quant<C, S, 1, false>(p, row_threads);
+  rmsnorm_quant<C, S, false>(p, row_threads);
 }
 
-// One vector a thread, 64 registers: eight warps a quarter of a multiprocessor
-// (two vectors and 80 registers, six warps: 160 us where this takes 138).
-constexpr int kAheadVecs = 1, kAheadRegs = 64, kAheadThreads = 1024;
+// 64 registers: eight warps a quarter of a multiprocessor.  (Two vectors a thread
+// and 80 registers, six warps: 160 us for 16384 x 7168 where this takes 138.)
+constexpr int kAheadRegs = 64;
 
 template <Codes C, Scales S>
 __global__ void __maxnreg__(kAheadRegs) rmsnorm_quant_rows_kernel(const Params p, int row_threads) {
-  rmsnorm_quant<C, S, kAheadVecs, true>(p, row_threads);
+  rmsnorm_quant<C, S, true>(p, row_threads);
 }
 
 // Longer rows: h is read again (from L2) for the second pass, and with a scale
@@ -319,20 +295,28 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_long_kernel(const P
   ss = row_sum(ss, red[0], warps);
   const float rstd = rstd_of(p, ss);
   if (t == 0 && p.rstd) p.rstd[row] = rstd;
-  quant::GroupScale rg;
-  if (C != Codes::kE2M1 && p.group == 0) {
+  const bool whole = C != Codes::kE2M1 && p.group == 0;
+  quant::GroupScale g;
+  if (whole) {
     uint32_t m = 0;
     for (int k = t * kVec; k < p.channels; k += step) {
       Pairs y;
       m = max(m, norm_vec(p, load_vec(hb, k), k, rstd, y));
     }
-    rg = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[1]), warps), d);
-    if (t == 0) store_scale<C, S>(p, row, 0, rg);
+    g = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[1]), warps), d);
+    if (t == 0) store_scale<C, S>(p, row, 0, g);
   }
-  for (int k0 = 0; k0 < p.channels; k0 += step) {
+  for (int k0 = 0; k0 < p.channels; k0 += step) {   // (all lanes of a warp: they reduce together)
     const int k = k0 + t * kVec;
-    const bool act = k < p.channels;
-    finish<C, S>(p, row, k, act, t, act ? load_vec(hb, k) : Vec{}, rstd, d, rg);
+    const bool on = k < p.channels;
+    Pairs y = {};
+    const uint32_t m = on ? norm_vec(p, load_vec(hb, k), k, rstd, y) : 0;
+    if (!whole) g = quant::group_scale<C, S>(group_max<C, S>(p.group, m), d);
+    if (on) {
+      const int32_t begun = whole ? -1 : group_begun<C, S>(p.group, k);
+      if (begun >= 0) store_scale<C, S>(p, row, begun, g);
+      store_codes<C, S>(p, row, k, y, g);
+    }
   }
   pad_scales<C>(p, row, t);
 }
