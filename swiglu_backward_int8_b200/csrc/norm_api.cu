@@ -76,6 +76,10 @@ int launch(const void* kernel, dim3 grid, dim3 block, cudaStream_t stream, void*
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
+// Threads of a row of `vecs` vectors where several rows share a CTA: 4, 8 or 16
+// lanes, or whole warps.
+int threads_of(int vecs) { return vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : round_up(vecs, 32); }
+
 // CTAs of `threads` threads with `regs` registers each that a multiprocessor
 // holds: each quarter of it has 16384 registers and takes every fourth warp.
 int ctas_per_sm(int threads, int regs) {
@@ -154,7 +158,7 @@ int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t
   // A vector a thread.  Few rows: each its own CTA.  Many: a persistent grid,
   // the next row loaded ahead.  Rows that no CTA holds: read again.
   const Variant v = vecs > sdq::norm::kMaxThreads ? Variant::kLong : rows <= sms ? Variant::kFew : Variant::kMany;
-  int row_threads = v == Variant::kLong ? sdq::norm::kMaxThreads : round_up(vecs, 32);
+  int row_threads = v == Variant::kLong ? sdq::norm::kMaxThreads : v == Variant::kMany ? threads_of(vecs) : round_up(vecs, 32);
   const int rows_cta = v == Variant::kMany ? std::max(1, 128 / row_threads) : 1;
   int64_t grid = (rows + rows_cta - 1) / rows_cta;
   if (v == Variant::kMany)
@@ -222,7 +226,7 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
   p.weight_f32 = format & SDQ_FMT_WEIGHT_F32 ? 1 : 0;
   const int vecs = static_cast<int>((channels + 7) / 8);
   const int kv = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
-  int row_threads = kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
+  int row_threads = kv == 1 ? threads_of(vecs) : kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
   const int rows_cta = kv == 1 ? std::max(1, 256 / row_threads) : 1;
   const int threads = row_threads * rows_cta;
   const int per_sm = kv ? std::min(4, ctas_per_sm(threads, sdq::norm::backward_regs(kv))) : 1;

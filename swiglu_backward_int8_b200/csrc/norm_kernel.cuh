@@ -42,13 +42,14 @@ struct Params {
   float eps;
 };
 
-// Sum (or, as bit patterns, largest) over the threads of one row.
-// red: one word per warp of the CTA.
-__device__ __forceinline__ float row_sum(float v, float* red, int row_warps) {
+// Sum (or, as bit patterns, largest) over the threads of one row: 4, 8 or 16
+// lanes, or whole warps.  red: one word per warp of the CTA.
+__device__ __forceinline__ float row_sum(float v, float* red, int row_threads) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if (row_warps == 1) return v;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int d = 16; d > 0; d >>= 1)
+    if (d < row_threads) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if (row_threads <= 32) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row_warps = row_threads >> 5;
   if (lane == 0) red[warp] = v;
   __syncthreads();
   const int first = warp / row_warps * row_warps;
@@ -58,10 +59,12 @@ __device__ __forceinline__ float row_sum(float v, float* red, int row_warps) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, int row_warps) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if (row_warps == 1) return v;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, int row_threads) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    if (d < row_threads) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+  if (row_threads <= 32) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row_warps = row_threads >> 5;
   if (lane == 0) red[warp] = v;
   __syncthreads();
   const int first = warp / row_warps * row_warps;
@@ -167,7 +170,8 @@ __device__ __forceinline__ void store_scale(const Params& p, int64_t row, int32_
     p.s[row * p.ld_s + group] = static_cast<uint8_t>(g.byte);
 }
 
-// Threads [0, row_threads) of a CTA take its first row, and so on.  A thread
+// Threads [0, row_threads) of a CTA take its first row, and so on; short rows
+// share a warp.  A thread
 // holds a vector of 16 consecutive channels, the next thread the next 16, so a
 // group of 16 to 256 channels is 1 to 16 neighbouring lanes of a warp.
 
@@ -210,8 +214,10 @@ __device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) 
   __shared__ float red[2][2][32];
   grid_dependency_wait();   // inputs may come from the previous kernel in the stream
   grid_launch_dependents();
-  const int row_warps = row_threads >> 5, rows_cta = blockDim.x / row_threads;
+  const int rows_cta = blockDim.x / row_threads;
   const int t = threadIdx.x % row_threads, k = t * kVec;
+  // (a group of a short row has no more lanes than the row)
+  const int32_t group = min(p.group, row_threads * kVec);
   const bool in = k < p.channels;
   const quant::Divisor d = quant::divisor<C, S>(p.global);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_cta;
@@ -237,13 +243,13 @@ __device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) 
       ss = sumsq(h);
     }
     if (kAhead) load(row + stride);
-    ss = row_sum(ss, red[flip][0], row_warps);
+    ss = row_sum(ss, red[flip][0], row_threads);
     const float rstd = rstd_of(p, ss);
     if (on && t == 0 && p.rstd) p.rstd[row] = rstd;
     Pairs y = {};
     uint32_t m = on ? norm_vec(p, h, k, rstd, y) : 0;
     const bool whole = C != Codes::kE2M1 && p.group == 0;   // one scale a row
-    m = whole ? row_max(m, reinterpret_cast<uint32_t*>(red[flip][1]), row_warps) : group_max<C, S>(p.group, m);
+    m = whole ? row_max(m, reinterpret_cast<uint32_t*>(red[flip][1]), row_threads) : group_max<C, S>(group, m);
     flip ^= 1;
     const quant::GroupScale g = quant::group_scale<C, S>(m, d);
     if (on) {
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_long_kernel(const P
   __shared__ float red[2][32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = threadIdx.x, warps = blockDim.x >> 5, step = blockDim.x * kVec;
+  const int t = threadIdx.x, step = blockDim.x * kVec;
   const int64_t row = blockIdx.x;
   const quant::Divisor d = quant::divisor<C, S>(p.global);
   const uint8_t* hb = p.residual ? p.h + 2 * row * p.ld_h : p.x + 2 * row * p.ld_x;
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_long_kernel(const P
     }
     ss += sumsq(h);
   }
-  ss = row_sum(ss, red[0], warps);
+  ss = row_sum(ss, red[0], blockDim.x);
   const float rstd = rstd_of(p, ss);
   if (t == 0 && p.rstd) p.rstd[row] = rstd;
   const bool whole = C != Codes::kE2M1 && p.group == 0;
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_long_kernel(const P
       Pairs y;
       m = max(m, norm_vec(p, load_vec(hb, k), k, rstd, y));
     }
-    g = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[1]), warps), d);
+    g = quant::group_scale<C, S>(row_max(m, reinterpret_cast<uint32_t*>(red[1]), blockDim.x), d);
     if (t == 0) store_scale<C, S>(p, row, 0, g);
   }
   for (int k0 = 0; k0 < p.channels; k0 += step) {   // (all lanes of a warp: they reduce together)
@@ -399,7 +405,7 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr bool kSeveral = kVecs == 1;
-  const int row_threads = kSeveral ? threads : blockDim.x, row_warps = row_threads >> 5;
+  const int row_threads = kSeveral ? threads : blockDim.x;
   const int rows_cta = kSeveral ? blockDim.x / row_threads : 1;
   const int t = kSeveral ? threadIdx.x % row_threads : threadIdx.x, mine = kSeveral ? threadIdx.x / row_threads : 0;
   const int64_t stride = static_cast<int64_t>(p.parts) * rows_cta;
@@ -440,7 +446,7 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads
       }
     }
     load(row + stride);
-    dot = row_sum(dot, red[flip], row_warps);
+    dot = row_sum(dot, red[flip], row_threads);
     flip ^= 1;
     const float c = backward_factor(p, rstd, dot);
 #pragma unroll
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_long_kernel(cons
   __shared__ float red[2][32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = threadIdx.x, warps = blockDim.x >> 5, step = blockDim.x * 8;
+  const int t = threadIdx.x, step = blockDim.x * 8;
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
   int flip = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_long_kernel(cons
     float dot = 0.0f;
     for (int k = t * 8; k < p.channels; k += step)
       dot += dot8(p, k, *reinterpret_cast<const uint4*>(gy + 2 * k), *reinterpret_cast<const uint4*>(h + 2 * k));
-    dot = row_sum(dot, red[flip], warps);
+    dot = row_sum(dot, red[flip], blockDim.x);
     flip ^= 1;
     const float c = backward_factor(p, rstd, dot);
     for (int k = t * 8; k < p.channels; k += step) {
