@@ -75,15 +75,18 @@ __global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const
   const int c16 = (t & 7) * 16;
   constexpr int kStep = kThreads / 8, kPasses = kTile / kStep;   // rows of a pass
   uint4 va[kPasses], vb[kPasses];
+  // addresses go on by a pass's rows: a product of 64 bits each costs more than the loads
+  const uint8_t* x = p.x + 2 * ((m0 + (t >> 3)) * p.ld_x + k0 + c16);
+  uint8_t* q = kRows ? p.q + (m0 + (t >> 3)) * p.ld_q + ((k0 + c16) >> 1) : nullptr;
+  const int rows_here = c16 < nch ? nrows - (t >> 3) : 0;   // rows of this thread's pass 0 to the last
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const int r = (t >> 3) + i * kStep;
     va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-    if (r < nrows && c16 < nch) {
-      const uint4* q = reinterpret_cast<const uint4*>(p.x + 2 * ((m0 + r) * p.ld_x + k0 + c16));
-      va[i] = q[0];
-      vb[i] = q[1];
+    if (i * kStep < rows_here) {
+      va[i] = reinterpret_cast<const uint4*>(x)[0];
+      vb[i] = reinterpret_cast<const uint4*>(x)[1];
     }
+    x += 2 * kStep * p.ld_x;
   }
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
@@ -102,9 +105,10 @@ __global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const
       uint32_t m = max(quant::amax(y), quant::amax(z));
       if (G == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       const quant::GroupScale gs = quant::group_scale<Codes::kE2M1, S>(m, d);
-      if (r < nrows && c16 < nch)
-        *reinterpret_cast<uint2*>(p.q + (m0 + r) * p.ld_q + ((k0 + c16) >> 1)) =
+      if (i * kStep < rows_here)
+        *reinterpret_cast<uint2*>(q) =
             make_uint2(quant::codes8<Codes::kE2M1, S>(y, gs).x, quant::codes8<Codes::kE2M1, S>(z, gs).x);
+      q += kStep * p.ld_q;
       const int grp = c16 / G;
       if ((c16 & (G - 1)) == 0)
         sc[(grp >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (grp & 3)] = static_cast<uint8_t>(c16 < nch ? gs.byte : 0u);
@@ -202,8 +206,8 @@ __device__ __forceinline__ uint4 values8(uint32_t w, float unit) {
 // What a code of 1 stands for, from a scale's byte.
 template <Scales S>
 __device__ __forceinline__ float unit_of(uint32_t b, float g) {
-  if (S == Scales::kE8M0) return b == 255 ? __uint_as_float(0x7FC00000u) : quant::exp2i(static_cast<int>(b) - 127);
-  return (b & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : __fmul_rn(quant::e4m3_value(b), g);
+  if (S == Scales::kE8M0) return b == 255 ? __uint_as_float(0x7FC00000u) : b == 0 ? quant::exp2i(-127) : __uint_as_float(b << 23);
+  return __fmul_rn(quant::e4m3_value(b), g);   // (a NaN byte is a NaN)
 }
 
 // A warp takes 256 channels of kDequantRows rows, a lane 8 of them.
@@ -219,18 +223,24 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantParam
   const int k = (blockIdx.x - strip * p.grid_k) * kDequantCols + (threadIdx.x & 31) * 8;
   const int64_t row0 = static_cast<int64_t>(strip) * (kThreads / 32 * kDequantRows) + (threadIdx.x >> 5) * kDequantRows;
   if (k >= p.channels) return;
+  const uint8_t* q = p.q + row0 * p.ld_q + (k >> 1);
+  const uint8_t* s = p.s + quant::tiled_scale(row0, k / G, p.tiles_k);   // a row on: 16 bytes (they share 32 rows)
+  uint8_t* out = p.out + 2 * (row0 * p.ld_out + k);
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kDequantRows), p.rows - row0));
   uint32_t w[kDequantRows], b[kDequantRows];
 #pragma unroll
   for (int i = 0; i < kDequantRows; ++i) {
-    if (row0 + i < p.rows) {
-      w[i] = *reinterpret_cast<const uint32_t*>(p.q + (row0 + i) * p.ld_q + (k >> 1));
-      b[i] = p.s[quant::tiled_scale(row0 + i, k / G, p.tiles_k)];
+    if (i < rows) {
+      w[i] = *reinterpret_cast<const uint32_t*>(q);
+      b[i] = s[16 * i];
     }
+    q += p.ld_q;
   }
 #pragma unroll
-  for (int i = 0; i < kDequantRows; ++i)
-    if (row0 + i < p.rows)
-      *reinterpret_cast<uint4*>(p.out + 2 * ((row0 + i) * p.ld_out + k)) = values8(w[i], unit_of<S>(b[i], g));
+  for (int i = 0; i < kDequantRows; ++i) {
+    if (i < rows) *reinterpret_cast<uint4*>(out) = values8(w[i], unit_of<S>(b[i], g));
+    out += 2 * p.ld_out;
+  }
 }
 
 }  // namespace fp4

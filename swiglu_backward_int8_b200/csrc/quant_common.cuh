@@ -92,11 +92,13 @@ __device__ __forceinline__ int ceil_exp(float t) {
 // One E4M3 byte (round to nearest even, saturated to 448).
 __device__ __forceinline__ uint32_t e4m3_byte(float v) { return e4m3x4(v, 0.0f, 0.0f, 0.0f) & 0xFFu; }
 
-// The value of a finite E4M3 byte.
+// The value of an E4M3 byte.
 __device__ __forceinline__ float e4m3_value(uint32_t b) {
-  const uint32_t e = (b >> 3) & 15u, m = b & 7u;
-  const float v = e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : static_cast<float>(m) * 0.001953125f;
-  return (b & 0x80u) ? -v : v;
+  uint32_t h;
+  float v;
+  asm("{\n\t.reg .b16 b;\n\tcvt.u16.u32 b, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n}\n" : "=r"(h) : "r"(b));
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n}\n" : "=f"(v) : "r"(h));
+  return v;
 }
 
 // Eight floats -> eight E2M1 codes (nearest even, saturated to 6), the first
@@ -196,9 +198,7 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, const Divi
     r.inv = __uint_as_float((254u - r.byte) << 23);
   } else {
     r.byte = max(e4m3_byte(t), 1u);
-    uint32_t h;
-    asm("{\n\t.reg .b16 b;\n\tcvt.u16.u32 b, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n}\n" : "=r"(h) : "r"(r.byte));
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n}\n" : "=f"(r.scale) : "r"(h));
+    r.scale = e4m3_value(r.byte);
     r.unit = __fmul_rn(r.scale, v.g);
     r.inv = reciprocal(r.unit);
   }
