@@ -49,7 +49,7 @@ def nvcc() -> str:
 def _run(cmd, verbose: bool) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"compiling failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     if verbose:
         sys.stderr.write(r.stdout + r.stderr)
 

@@ -286,3 +286,54 @@ def test_product_large():
         want, mag = av @ bv.t(), av.abs() @ bv.abs().t()
         # the values read back are bf16: exact for E8M0 scales and for E4M3 ones (four and three bits)
         assert ((got - want).abs() <= (k / 16 + 2) * 2.0 ** -23 * mag + 2.0 ** -8 * want.abs()).all()
+
+
+# ---- the product with more tiles than the device takes at once ---------------------
+#
+# (the form that two multiprocessors share: 256 x 256 outputs, a persistent grid)
+
+def _gpu_operand(rng, rows, k, scales, **kw):
+    q, s, v = _operand(rng, rows, k, scales, **kw)
+    return q, s, v.cuda()
+
+
+@pytest.mark.parametrize("scales", ["e8m0", "e4m3"])
+@pytest.mark.parametrize("m,n,k", [(1665, 1537, 32), (1537, 1665, 96), (1700, 1800, 288), (2561, 1280, 544), (130, 20000, 160),
+                                   (20000, 130, 2080), (1664, 1664, 1312)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product_of_many_tiles(scales, m, n, k, dtype):
+    rng = np.random.default_rng(m + k)
+    a, a_s, av = _gpu_operand(rng, m, k, scales, nan_row=m - 2)
+    b, b_s, bv = _gpu_operand(rng, n, k, scales)
+    ga, gb = (torch.tensor([0.37], device="cuda"), None) if scales == "e4m3" else (None, None)
+    out = U.Guarded((m, n), dtype, -77.0)
+    sdq.matmul_fp4(a, a_s, b, b_s, a_global=ga, b_global=gb, out=out.t)
+    torch.cuda.synchronize()
+    assert sdq.sdq_device_status() == 0 and out.guards_intact()
+    alpha = 1.0 if ga is None else float(ga.double())
+    want, mag = (av @ bv.t()) * alpha, (av.abs() @ bv.abs().t()) * alpha
+    got = out.t.double()
+    tol = (k / 16 + 2) * 2.0 ** -23 * mag + (2.0 ** -8 * want.abs() if dtype == torch.bfloat16 else 0)
+    assert ((got - want).abs() <= tol)[torch.arange(m) != m - 2].all()
+    assert got[m - 2].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [1672, 1665])
+def test_product_of_many_tiles_strided_and_exact(dtype, n):
+    """Whole numbers (exact in fp32, and in bf16 up to 256), rows of the output that start on 16 bytes and that do not."""
+    rng = np.random.default_rng(n)
+    m, k = 1700, 64
+    ints = np.array([0, 2, 4, 10, 12])                     # 0, 1, 2, -1, -2: sums within 64 * 4 = 256
+    ca, cb = ints[rng.integers(0, 5, (m, k))], ints[rng.integers(0, 5, (n, k))]
+    t = lambda r: torch.from_numpy(R.tiles(np.full((r, 2), 127))).cuda().view(_DT["e8m0"])  # noqa: E731
+    out = torch.full((m, n + 8), 9.0, dtype=dtype, device="cuda")
+    view = out[:, 8:] if n == 1672 else out[:, 3:n + 3]
+    sdq.matmul_fp4(torch.from_numpy(R.pack(ca)).cuda(), t(m), torch.from_numpy(R.pack(cb)).cuda(), t(n), out=view)
+    want = torch.from_numpy(R.e2m1_value(ca) @ R.e2m1_value(cb).T).cuda()
+    assert torch.equal(view.double(), want)
+    rest = torch.ones_like(out, dtype=torch.bool)
+    rest[:, 8:] = n != 1672
+    if n != 1672:
+        rest[:, 3:n + 3] = False
+    assert (out[rest] == 9).all()
