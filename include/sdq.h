@@ -324,6 +324,7 @@ int sdq_validate_swiglu_q8_1(const void* gate, int64_t ld_gate, const void* up, 
 #define SDQ_FMT_WEIGHT_F32 32u
 #define SDQ_FMT_OUT_F32 64u
 #define SDQ_FP4_K_MULTIPLE 32
+#define SDQ_MAX_LD_NORM ((1LL << 32) - 16) /* largest leading dimension of the norm's arrays */
 
 /*
  * sdq_rmsnorm_quant -- RMS norm with the residual's addition, its rows
@@ -350,7 +351,9 @@ int sdq_validate_swiglu_q8_1(const void* gate, int64_t ld_gate, const void* up, 
  *             not (fp32 scales), for E2M1 exactly one of SDQ_FMT_E8M0 and
  *             SDQ_FMT_SCALE_E4M3; SDQ_FMT_WEIGHT_F32
  *   rows 0 <= rows <= SDQ_MAX_M (0: no-op); channels a multiple of
- *   SDQ_K_MULTIPLE (E2M1: SDQ_FP4_K_MULTIPLE), at most SDQ_MAX_K.
+ *   SDQ_K_MULTIPLE (E2M1: SDQ_FP4_K_MULTIPLE), at most SDQ_MAX_K; leading
+ *   dimensions at most SDQ_MAX_LD_NORM.
+ * Sums are fp32: a row whose squares add up past 3.4e38 has rstd 0.
  * One kernel on `stream`; allocates nothing.  Errors as sdq_fuse_strided.
  */
 int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,

@@ -55,7 +55,7 @@ bool misaligned(const void* p, uintptr_t mask) { return reinterpret_cast<uintptr
 
 // A bf16 array of rows: unset, or its stride and alignment right.
 int check_rows(const void* p, int64_t ld, int64_t channels) {
-  if (ld < channels || ld > SDQ_MAX_LD) return SDQ_ERR_STRIDE;
+  if (ld < channels || ld > SDQ_MAX_LD_NORM) return SDQ_ERR_STRIDE;
   return misaligned(p, 15) || (ld & 7) ? SDQ_ERR_ALIGN : SDQ_OK;
 }
 
@@ -110,10 +110,10 @@ int sdq_validate_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual
   if (st == SDQ_OK && y) st = check_rows(y, ld_y, channels);
   if (st != SDQ_OK) return st;
   const int64_t qbytes = e2m1 ? channels / 2 : channels;
-  if (ld_q < qbytes || ld_q > SDQ_MAX_LD) return SDQ_ERR_STRIDE;
+  if (ld_q < qbytes || ld_q > SDQ_MAX_LD_NORM) return SDQ_ERR_STRIDE;
   if (!e2m1) {
     const int64_t g = group_size ? group_size : channels;
-    if (ld_s < (channels + g - 1) / g || ld_s > SDQ_MAX_LD) return SDQ_ERR_STRIDE;
+    if (ld_s < (channels + g - 1) / g || ld_s > SDQ_MAX_LD_NORM) return SDQ_ERR_STRIDE;
   }
   if (misaligned(q, 15) || (ld_q & 15) || misaligned(weight, 15) || misaligned(rstd, 3) || misaligned(global_scale, 3))
     return SDQ_ERR_ALIGN;
@@ -142,18 +142,19 @@ int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t
   p.rstd = rstd;
   p.global = global_scale;
   p.rows = rows;
-  p.ld_x = ld_x;
-  p.ld_residual = ld_residual;
-  p.ld_h = ld_h;
-  p.ld_q = ld_q;
-  p.ld_s = ld_s;
-  p.ld_y = ld_y;
+  p.ld_x = static_cast<uint32_t>(ld_x);
+  p.ld_residual = static_cast<uint32_t>(ld_residual);
+  p.ld_h = static_cast<uint32_t>(ld_h);
+  p.ld_q = static_cast<uint32_t>(ld_q);
+  p.ld_s = static_cast<uint32_t>(ld_s);
+  p.ld_y = static_cast<uint32_t>(ld_y);
   p.channels = static_cast<int32_t>(channels);
   p.group = group_size;
   p.groups = groups;
   p.tiles_k = (groups + 3) / 4;
   p.weight_f32 = format & SDQ_FMT_WEIGHT_F32 ? 1 : 0;
   p.eps = eps;
+  p.inv_channels = 1.0f / static_cast<float>(channels);
   const int vecs = static_cast<int>(channels / sdq::norm::kVec);
   // A vector a thread.  Few rows: each its own CTA.  Many: a persistent grid,
   // the next row loaded ahead.  Rows that no CTA holds: read again.
@@ -218,11 +219,12 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
   p.gw = grad_weight;
   p.part = static_cast<float*>(workspace);
   p.rows = rows;
-  p.ld_gy = ld_grad_y;
-  p.ld_h = ld_h;
-  p.ld_gh = ld_grad_h;
-  p.ld_gx = ld_grad_x;
+  p.ld_gy = static_cast<uint32_t>(ld_grad_y);
+  p.ld_h = static_cast<uint32_t>(ld_h);
+  p.ld_gh = static_cast<uint32_t>(ld_grad_h);
+  p.ld_gx = static_cast<uint32_t>(ld_grad_x);
   p.channels = static_cast<int32_t>(channels);
+  p.inv_channels = 1.0f / static_cast<float>(channels);
   p.weight_f32 = format & SDQ_FMT_WEIGHT_F32 ? 1 : 0;
   const int vecs = static_cast<int>((channels + 7) / 8);
   const int kv = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;

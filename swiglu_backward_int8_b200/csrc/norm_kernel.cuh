@@ -35,12 +35,18 @@ struct Params {
   uint8_t* y;                // bf16 or null
   float* rstd;               // [rows] or null
   const float* global;       // the scale per tensor (E4M3 scales) or null
-  int64_t rows, ld_x, ld_residual, ld_h, ld_q, ld_s, ld_y;
+  int64_t rows;
+  uint32_t ld_x, ld_residual, ld_h, ld_q, ld_s, ld_y;   // (a row's offset is one 32 x 32 -> 64 bit product)
   int32_t channels, group, groups;   // group 0: the whole row
   int32_t tiles_k;                   // scale tiles along the channels (E2M1)
   int32_t weight_f32;
-  float eps;
+  float eps, inv_channels;
 };
+
+// The offset of a row, in elements.
+__device__ __forceinline__ int64_t at(int64_t row, uint32_t ld) {
+  return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(row)) * ld);
+}
 
 // Sum (or, as bit patterns, largest) over the threads of one row: 4, 8 or 16
 // lanes, or whole warps.  red: one word per warp of the CTA.
@@ -152,12 +158,12 @@ __device__ __forceinline__ void store_codes(const Params& p, int64_t row, int32_
                                             const quant::GroupScale& g) {
   const uint2 a = quant::codes8<C, S>(*reinterpret_cast<const float2(*)[4]>(&y[0]), g);
   const uint2 b = quant::codes8<C, S>(*reinterpret_cast<const float2(*)[4]>(&y[4]), g);
-  uint8_t* q = p.q + row * p.ld_q;
+  uint8_t* q = p.q + at(row, p.ld_q);
   if (C == Codes::kE2M1)
     *reinterpret_cast<uint2*>(q + (k >> 1)) = make_uint2(a.x, b.x);
   else
     *reinterpret_cast<uint4*>(q + k) = make_uint4(a.x, a.y, b.x, b.y);
-  if (p.y) store_vec(p.y + 2 * row * p.ld_y, k, pack(y));
+  if (p.y) store_vec(p.y + 2 * at(row, p.ld_y), k, pack(y));
 }
 
 template <Codes C, Scales S>
@@ -165,9 +171,9 @@ __device__ __forceinline__ void store_scale(const Params& p, int64_t row, int32_
   if (C == Codes::kE2M1)
     p.s[quant::tiled_scale(row, group, p.tiles_k)] = static_cast<uint8_t>(g.byte);
   else if (S == Scales::kF32)
-    reinterpret_cast<float*>(p.s)[row * p.ld_s + group] = g.scale;
+    reinterpret_cast<float*>(p.s)[at(row, p.ld_s) + group] = g.scale;
   else
-    p.s[row * p.ld_s + group] = static_cast<uint8_t>(g.byte);
+    p.s[at(row, p.ld_s) + group] = static_cast<uint8_t>(g.byte);
 }
 
 // Threads [0, row_threads) of a CTA take its first row, and so on; short rows
@@ -195,8 +201,13 @@ __device__ __forceinline__ int32_t group_begun(int32_t group, int32_t k) {
   return (k & (group - 1)) ? -1 : k >> shift;
 }
 
+// 1 / sqrt(mean + eps): the hardware's approximation (2^-22) and one Newton step.
 __device__ __forceinline__ float rstd_of(const Params& p, float ss) {
-  return __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(p.channels)) + p.eps);
+  const float v = fmaf(ss, p.inv_channels, p.eps);
+  if (!(v > 1e-36f && v < 1e36f)) return __frsqrt_rn(v);   // zero, tiny, huge, not finite
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return fmaf(fmaf(v * r, -r, 1.0f) * 0.5f, r, r);
 }
 
 // Groups that pad the last scale tile: zero, as the product multiplies them
@@ -225,8 +236,8 @@ __device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) 
   Vec x = {}, r = {};
   auto load = [&](int64_t from) {
     if (from >= p.rows || !in) return;
-    x = load_vec(p.x + 2 * from * p.ld_x, k);
-    if (p.residual) r = load_vec(p.residual + 2 * from * p.ld_residual, k);
+    x = load_vec(p.x + 2 * at(from, p.ld_x), k);
+    if (p.residual) r = load_vec(p.residual + 2 * at(from, p.ld_residual), k);
   };
   load(row);
   int flip = 0;
@@ -238,7 +249,7 @@ __device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) 
       h = x;
       if (p.residual) {
         h = {add_bf16x8(x.a, r.a), add_bf16x8(x.b, r.b)};
-        store_vec(p.h + 2 * row * p.ld_h, k, h);
+        store_vec(p.h + 2 * at(row, p.ld_h), k, h);
       }
       ss = sumsq(h);
     }
@@ -287,14 +298,14 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_long_kernel(const P
   const int t = threadIdx.x, step = blockDim.x * kVec;
   const int64_t row = blockIdx.x;
   const quant::Divisor d = quant::divisor<C, S>(p.global);
-  const uint8_t* hb = p.residual ? p.h + 2 * row * p.ld_h : p.x + 2 * row * p.ld_x;
+  const uint8_t* hb = p.residual ? p.h + 2 * at(row, p.ld_h) : p.x + 2 * at(row, p.ld_x);
   float ss = 0.0f;
   for (int k = t * kVec; k < p.channels; k += step) {
-    Vec h = load_vec(p.x + 2 * row * p.ld_x, k);
+    Vec h = load_vec(p.x + 2 * at(row, p.ld_x), k);
     if (p.residual) {
-      const Vec r = load_vec(p.residual + 2 * row * p.ld_residual, k);
+      const Vec r = load_vec(p.residual + 2 * at(row, p.ld_residual), k);
       h = {add_bf16x8(h.a, r.a), add_bf16x8(h.b, r.b)};
-      store_vec(p.h + 2 * row * p.ld_h, k, h);
+      store_vec(p.h + 2 * at(row, p.ld_h), k, h);
     }
     ss += sumsq(h);
   }
@@ -338,8 +349,10 @@ struct BwdParams {
   uint8_t* gx;             // bf16 rows
   float* gw;               // [channels]
   float* part;             // [parts, channels] partial sums of gw
-  int64_t rows, ld_gy, ld_h, ld_gh, ld_gx;
+  int64_t rows;
+  uint32_t ld_gy, ld_h, ld_gh, ld_gx;
   int32_t channels, weight_f32, parts;
+  float inv_channels;
 };
 
 // CTA b takes rows b, b + parts, ... and adds their grad_y n to its own row of
@@ -390,7 +403,7 @@ __device__ __forceinline__ float dot8(const BwdParams& p, int32_t k, const uint4
 
 // rstd^3 mean(grad_y w h), from the row's sum.
 __device__ __forceinline__ float backward_factor(const BwdParams& p, float rstd, float dot) {
-  return rstd * rstd * (rstd * __fdiv_rn(dot, static_cast<float>(p.channels)));
+  return rstd * rstd * (rstd * (dot * p.inv_channels));
 }
 
 // Rows that fit the registers, kVecs vectors a thread: grad_y and h of the next
@@ -413,8 +426,8 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads
   uint4 gn[kVecs], hn[kVecs];
   auto load = [&](int64_t row) {
     if (row >= p.rows) return;
-    const uint8_t* gy = p.gy + 2 * row * p.ld_gy;
-    const uint8_t* h = p.h + 2 * row * p.ld_h;
+    const uint8_t* gy = p.gy + 2 * at(row, p.ld_gy);
+    const uint8_t* h = p.h + 2 * at(row, p.ld_h);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int k = (t + i * row_threads) * 8;
@@ -430,8 +443,8 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows_cta; base < p.rows; base += stride, row += stride) {
     const bool on = !kSeveral || row < p.rows;
     const float rstd = on ? p.rstd[row] : 0.0f;
-    const uint8_t* gh = p.gh ? p.gh + 2 * row * p.ld_gh : nullptr;
-    uint8_t* gx = p.gx + 2 * row * p.ld_gx;
+    const uint8_t* gh = p.gh ? p.gh + 2 * at(row, p.ld_gh) : nullptr;
+    uint8_t* gx = p.gx + 2 * at(row, p.ld_gx);
     uint4 gv[kVecs], hv[kVecs], rv[kVecs];
     float dot = 0.0f;
 #pragma unroll
@@ -494,9 +507,9 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_long_kernel(cons
   int flip = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
     const float rstd = p.rstd[row];
-    const uint8_t *gy = p.gy + 2 * row * p.ld_gy, *h = p.h + 2 * row * p.ld_h;
-    const uint8_t* gh = p.gh ? p.gh + 2 * row * p.ld_gh : nullptr;
-    uint8_t* gx = p.gx + 2 * row * p.ld_gx;
+    const uint8_t *gy = p.gy + 2 * at(row, p.ld_gy), *h = p.h + 2 * at(row, p.ld_h);
+    const uint8_t* gh = p.gh ? p.gh + 2 * at(row, p.ld_gh) : nullptr;
+    uint8_t* gx = p.gx + 2 * at(row, p.ld_gx);
     float dot = 0.0f;
     for (int k = t * 8; k < p.channels; k += step)
       dot += dot8(p, k, *reinterpret_cast<const uint4*>(gy + 2 * k), *reinterpret_cast<const uint4*>(h + 2 * k));
