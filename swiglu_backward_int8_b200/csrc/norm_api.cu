@@ -227,18 +227,21 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
   p.inv_channels = 1.0f / static_cast<float>(channels);
   p.weight_f32 = format & SDQ_FMT_WEIGHT_F32 ? 1 : 0;
   const int vecs = static_cast<int>((channels + 7) / 8);
-  const int kv = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
-  int row_threads = kv == 1 ? threads_of(vecs) : kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
-  const int rows_cta = kv == 1 ? std::max(1, 256 / row_threads) : 1;
+  // Vectors a thread, and rows a CTA: several short ones.
+  const int kv = vecs <= 16 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
+  const bool several = vecs <= 256;
+  int row_threads = several ? threads_of((vecs + kv - 1) / kv) : kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
+  const int rows_cta = several ? std::max(1, 256 / row_threads) : 1;
   const int threads = row_threads * rows_cta;
   const int per_sm = kv ? std::min(4, ctas_per_sm(threads, sdq::norm::backward_regs(kv))) : 1;
   p.parts = static_cast<int32_t>(
       std::min<int64_t>((rows + rows_cta - 1) / rows_cta, std::min<int64_t>(kMaxParts, int64_t{sms} * per_sm)));
   const void* k = kv == 0   ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_long_kernel)
-                  : kv == 1 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<1>)
-                  : kv == 2 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<2>)
-                            : reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<4>);
-  // at most 256 / row_threads rows of 8 row_threads channels: 8 KB
+                  : kv == 1 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<1, true>)
+                  : several ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<2, true>)
+                  : kv == 2 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<2, false>)
+                            : reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<4, false>);
+  // at most 256 / row_threads rows of 16 row_threads channels: 16 KB
   const size_t smem = rows_cta > 1 ? static_cast<size_t>(rows_cta) * channels * 4 : 0;
   void* args[] = {&p, &row_threads};
   if (const int e = launch(k, dim3(p.parts), dim3(threads), s, args, smem)) return e;

@@ -410,14 +410,13 @@ __device__ __forceinline__ float backward_factor(const BwdParams& p, float rstd,
 // row are loaded ahead, grad_h while the row's sum is added up.  Short rows go
 // several to a CTA (threads [0, row_threads) the first, and so on); its sums are
 // put together at the end, in the rows' order.
-// (kVecs above 1: one row, and the compiler knows.)
-template <int kVecs>
+// (kSeveral false: one row, and the compiler knows.)
+template <int kVecs, bool kSeveral>
 __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads) {
   __shared__ float red[2][32];
   extern __shared__ float sums[];   // [rows of the CTA][channels], for several rows
   grid_dependency_wait();
   grid_launch_dependents();
-  constexpr bool kSeveral = kVecs == 1;
   const int row_threads = kSeveral ? threads : blockDim.x;
   const int rows_cta = kSeveral ? blockDim.x / row_threads : 1;
   const int t = kSeveral ? threadIdx.x % row_threads : threadIdx.x, mine = kSeveral ? threadIdx.x / row_threads : 0;
@@ -491,9 +490,9 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads
 // Registers a thread, and with them warps a quarter of a multiprocessor: 8, 6, 4.
 constexpr int backward_regs(int vecs) { return vecs == 1 ? 64 : vecs == 2 ? 80 : 128; }
 
-template <int kVecs>
+template <int kVecs, bool kSeveral>
 __global__ void __maxnreg__(backward_regs(kVecs)) rmsnorm_backward_kernel(const BwdParams p, int row_threads) {
-  rmsnorm_backward<kVecs>(p, row_threads);
+  rmsnorm_backward<kVecs, kSeveral>(p, row_threads);
 }
 
 // Longer rows: read twice, the sums of grad_y n in memory between rows (a
