@@ -72,21 +72,6 @@ const void* quantize_kernel(bool rows, bool cols) {
               : reinterpret_cast<const void*>(sdq::fp4::quantize_kernel<S, false, true>);
 }
 
-struct MatmulKernel {
-  const void* fn;
-  size_t smem;
-  int n;
-  SmemLimit* limit;
-};
-
-template <Scales S, int kN>
-MatmulKernel pair_of(bool f32) {
-  static SmemLimit limits[2];
-  return {f32 ? reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kN, true>)
-              : reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kN, false>),
-          sdq::mm4::PairShape<S, kN>::kSmem, kN, &limits[f32]};
-}
-
 // One call of the product, checked.
 struct Product {
   const void* a; int64_t ld_a; const void* a_s; const float* a_global;
@@ -97,7 +82,10 @@ struct Product {
   cudaStream_t stream;
 };
 
-int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
+// Many tiles: pairs of multiprocessors.
+template <Scales S, bool kF32>
+int launch_pair(const Product& c, int sms) {
+  using Z = sdq::mm4::PairShape<S>;
   const int64_t tiles_k = tiles_of(c.k, c.format);
   sdq::mm4::PairParams p = {};
   p.ga = c.a_global;
@@ -108,24 +96,24 @@ int launch_pair(const Product& c, const MatmulKernel& kern, int sms) {
   p.rows_b = c.n;
   p.codes = static_cast<int32_t>(c.k);
   p.tiles_a = static_cast<int32_t>((c.m + 255) / 256);
-  p.tiles_b = static_cast<int32_t>((c.n + kern.n - 1) / kern.n);
-  const bool f32 = c.format & SDQ_FMT_OUT_F32;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(c.out) | static_cast<uintptr_t>(c.ld_out * (f32 ? 4 : 2));
+  p.tiles_b = static_cast<int32_t>((c.n + sdq::mm4::kN - 1) / sdq::mm4::kN);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(c.out) | static_cast<uintptr_t>(c.ld_out * (kF32 ? 4 : 2));
   p.vec = at & 15 ? 0 : 1;
   p.wait_limit_ns = sdq_internal::wait_limit();
   if (const int e = sdq_internal::device_status_word(&p.status)) return e;
   CUtensorMap ma, mb, msa, msb, mo = {};
-  const uint32_t stage = c.format & SDQ_FMT_E8M0 ? 2 : 4;   // scale tiles a stage
   if (const int e = sdq_internal::make_code_map(&ma, c.a, c.k / 2, c.m, c.ld_a, 128)) return e;
-  if (const int e = sdq_internal::make_code_map(&mb, c.b, c.k / 2, c.n, c.ld_b, kern.n / 2)) return e;
-  if (const int e = sdq_internal::make_scale_map(&msa, c.a_s, tiles_k, (c.m + 127) / 128, stage)) return e;
-  if (const int e = sdq_internal::make_scale_map(&msb, c.b_s, tiles_k, (c.n + 127) / 128, stage)) return e;
+  if (const int e = sdq_internal::make_code_map(&mb, c.b, c.k / 2, c.n, c.ld_b, sdq::mm4::kN / 2)) return e;
+  if (const int e = sdq_internal::make_scale_map(&msa, c.a_s, tiles_k, (c.m + 127) / 128, Z::kScaleTiles)) return e;
+  if (const int e = sdq_internal::make_scale_map(&msb, c.b_s, tiles_k, (c.n + 127) / 128, Z::kScaleTiles)) return e;
   if (p.vec)
-    if (const int e = sdq_internal::make_out_map(&mo, c.out, f32, c.n, c.m, c.ld_out)) return e;
-  if (const int e = kern.limit->set(kern.fn, static_cast<int>(kern.smem))) return e;
+    if (const int e = sdq_internal::make_out_map(&mo, c.out, kF32, c.n, c.m, c.ld_out)) return e;
+  const void* fn = reinterpret_cast<const void*>(sdq::mm4::matmul_pair_kernel<S, kF32>);
+  static SmemLimit limit;
+  if (const int e = limit.set(fn, static_cast<int>(Z::kSmem))) return e;
   const int64_t pairs = std::min<int64_t>(sms / 2, int64_t{p.tiles_a} * p.tiles_b);
   void* args[] = {&ma, &mb, &msa, &msb, &mo, &p};
-  return launch(kern.fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kPairThreads, kern.smem, c.stream, args);
+  return launch(fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kPairThreads, Z::kSmem, c.stream, args);
 }
 
 // Few rows of a, or few tiles: clusters that share the steps along k.
@@ -292,7 +280,8 @@ int sdq_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_
   // multiprocessors busy than 256 x 256 outputs a pair (256 x 1024 x 1024: 5.1 us
   // instead of 5.7; 1024 x 1024 x 4096: 9.4 instead of 9.8).
   if (m <= 128 || (m + 127) / 128 * ((n + 127) / 128) <= sms) return e8m0 ? launch_strip<Scales::kE8M0>(c, sms) : launch_strip<Scales::kE4M3>(c, sms);
-  return launch_pair(c, e8m0 ? pair_of<Scales::kE8M0, 256>(f32) : pair_of<Scales::kE4M3, 256>(f32), sms);
+  if (f32) return e8m0 ? launch_pair<Scales::kE8M0, true>(c, sms) : launch_pair<Scales::kE4M3, true>(c, sms);
+  return e8m0 ? launch_pair<Scales::kE8M0, false>(c, sms) : launch_pair<Scales::kE4M3, false>(c, sms);
 }
 
 }  // extern "C"

@@ -9,7 +9,11 @@
 // tiles (128 rows x 4 groups, or the transposed ones), put together in shared
 // memory.
 //
-// 2 bytes are read and 0.53 or 0.56 written a value and axis; DRAM bounds it.
+// 2 bytes are read and 0.53 or 0.56 written a value and axis.  Along the rows DRAM
+// bounds it (8192 x 4096: 15 to 17 us, 77 to 85 % of the measured copy's rate);
+// along both axes instructions do, 18 a value (28 us, 57 %): the issue slots are
+// 62 % taken, the half-rate integer pipe, which unpacks, converts and compares,
+// nearly full.  Reading back: 15.3 us, 85 %.
 #pragma once
 
 #include <cstdint>

@@ -1,5 +1,5 @@
 // The large form of the product C = A B^T of two microscaled 4-bit operands
-// (fp4_matmul.cuh): two multiprocessors share a tile of 256 x kN outputs
+// (fp4_matmul.cuh): two multiprocessors share a tile of 256 x 256 outputs
 // (tcgen05.mma with cta_group::2), and a persistent grid of such pairs walks
 // the tiles, a tile's sums being read out while the next one is computed.
 //
@@ -8,10 +8,16 @@
 // cycle of it at the tensor cores' 4-bit rate, where a single CTA's 128 x 256
 // tile would read 96 and be refilled at 100 more.
 //
-// Tensor memory: two accumulators of kN columns and two sets of scales.  For
-// kN = 256 those do not fit, so the accumulators share columns: the second
-// starts where the first still has some to go, and the epilogue of either
-// reads those first and gives them back.
+// Tensor memory: two accumulators of 256 columns and two sets of scales do not
+// fit, so the accumulators share columns: the second starts where the first
+// still has some to go, and the epilogue of either reads those first and gives
+// them back.
+//
+// What bounds it: filling shared memory from L2.  A stage is 35 KB (38 with E4M3
+// scales) a multiprocessor, and 82 GB/s each (12 TB/s in all) is what the loads
+// reach with the products taken out: 170 of the 176 us of 8192 x 14336 x 4096 at
+// full clock (5.5 PFLOP/s).  Back to back for a second the power limit lowers the
+// clock: 205 us (4.7 PFLOP/s).
 #pragma once
 
 #include "fp4_matmul.cuh"
@@ -22,7 +28,9 @@ namespace mm4 {
 constexpr int kEpilogueWarps = 8;
 constexpr int kPairThreads = 64 + 32 * kEpilogueWarps;   // a load warp, an mma warp, the epilogue's
 
-template <Scales S, int kN>
+constexpr int kN = 256;   // columns of a tile
+
+template <Scales S>
 struct PairShape {
   static constexpr int kScaleTiles = S == Scales::kE8M0 ? 2 : 4;   // a stage's scale tiles per 128 rows
   static constexpr int kBlocksB = kN / 128;
@@ -36,11 +44,11 @@ struct PairShape {
   static constexpr int kColsScaleA = kScaleTiles * 4;
   static constexpr int kColsScale = kColsScaleA + kScaleTiles * 4 * kBlocksB;
   static constexpr int kScaleCol = 512 - 2 * kColsScale;
-  static constexpr int kAcc1 = 2 * kN <= kScaleCol ? kN : (kScaleCol - kN) / 64 * 64;   // the second accumulator's first column
+  static constexpr int kAcc1 = (kScaleCol - kN) / 64 * 64;   // the second accumulator's first column
   static constexpr int kShared = kN - kAcc1;                                // columns both accumulators use
   static constexpr size_t kSmem = 1024 + kStages * static_cast<size_t>(kStage) + kBoxes;
   static_assert(kStage % 1024 == 0, "the swizzled boxes start on 1024 bytes");
-  static_assert(kAcc1 >= 0 && kAcc1 % 64 == 0 && kShared % 64 == 0 && kShared <= 128,
+  static_assert(kAcc1 >= 0 && kAcc1 % 64 == 0 && kShared % 64 == 0 && kShared > 0 && kShared <= 128,
                 "whole pieces of 64 columns, those that are shared the first of a warp");
 };
 
@@ -166,12 +174,12 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const PairPara
 
 // ---- the kernel -----------------------------------------------------------------------
 
-template <Scales S, int kN, bool kF32>
+template <Scales S, bool kF32>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     matmul_pair_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                        const __grid_constant__ CUtensorMap msa, const __grid_constant__ CUtensorMap msb,
                        const __grid_constant__ CUtensorMap mo, const PairParams p) {
-  using Z = PairShape<S, kN>;
+  using Z = PairShape<S>;
   extern __shared__ uint8_t raw[];
   // full: the stage's loads of both CTAs (the first CTA's are waited on);
   // empty: the products that read the stage; sums: a tile's sums are complete;
@@ -248,11 +256,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       int n = 0, k = 0;   // loads, tiles so far
       bool ok = true;
       for (int t = first; t < tiles && ok; t += stride, ++k) {
-        if (Z::kShared > 0) {   // the tile before has given back the shared columns
-          if (k >= 1) ok = wait(sync, freed + 8 * ((k - 1) & 1), ((k - 1) >> 1) & 1);
-        } else {                // the tile before that is read out
-          if (k >= 2) ok = wait(sync, freed + 8 * (k & 1), ((k - 2) >> 1) & 1);
-        }
+        // the tile before has given back the shared columns (and the one before it all)
+        if (k >= 1) ok = wait(sync, freed + 8 * ((k - 1) & 1), ((k - 1) >> 1) & 1);
         fence_after();
         const uint32_t acc = tmem + ((k & 1) ? Z::kAcc1 : 0);
         for (int i = 0; i < steps && ok; ++i, ++n) {
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t row0 = k < 0 ? p.rows_a : static_cast<int64_t>(ta) * 256 + rank * 128 + quarter * 32;
       const int64_t col0 = static_cast<int64_t>(tb) * kN;
       const uint32_t acc = tmem + (k > 0 && (k & 1) ? Z::kAcc1 : 0) + lanes;
-      const int start = Z::kShared > 0 && (k & 1) == 0 ? Z::kAcc1 / 64 : 0;
-      if (Z::kShared > 0 && k >= 0 && half >= Z::kShared / 64) {   // none of its pieces is shared: it is done with the tile before
+      const int start = (k & 1) == 0 ? Z::kAcc1 / 64 : 0;
+      if (k >= 0 && half >= Z::kShared / 64) {   // none of its pieces is shared: it is done with the tile before
         __syncwarp();
         if (lane == 0) arrive_at(freed0 + 8 * (k & 1));
       }
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         load_sums32(acc + piece * 64, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
         load_sums32(acc + piece * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
         load_wait();
-        if (k >= 0 && (Z::kShared > 0 ? c < Z::kShared / 64 : c + 2 >= kPieces)) {
+        if (k >= 0 && c < Z::kShared / 64) {
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_at(freed0 + 8 * (k & 1));
