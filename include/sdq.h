@@ -385,7 +385,8 @@ int sdq_validate_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual
  *   workspace      device memory of sdq_rmsnorm_backward_workspace_bytes(rows,
  *                  channels) bytes, 16-byte aligned; calls that overlap (on other
  *                  streams, or two graphs replayed at once) need one each
- * Two kernels on `stream`, without atomics: equal inputs give equal bits.
+ * One kernel on `stream`, or two for long calls, without atomics: equal inputs give
+ * equal bits.
  */
 int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, int64_t ld_h,
                          const void* weight, const float* rstd, const void* grad_h, int64_t ld_grad_h,

@@ -18,7 +18,7 @@
 // the measured copy's rate; the backward of 16384 x 4096, 92 us, 89 %, of 16384 x
 // 7168, 190 us, 76 % (14 warps a multiprocessor, by registers).  Short calls are
 // bound by the row's latency (load, sum over the CTA, scale, store) and the
-// launch: 1 x 7168, 2.9 us; the backward of 517 x 7168, 11.5 us in two kernels.
+// launch: 1 x 7168, 2.9 us; the backward of 517 x 7168, 9.2 us.
 #pragma once
 
 #include <cstdint>
@@ -501,6 +501,83 @@ constexpr int backward_regs(int vecs) { return vecs == 1 ? 64 : vecs == 2 ? 80 :
 template <int kVecs, bool kSeveral>
 __global__ void __maxnreg__(backward_regs(kVecs)) rmsnorm_backward_kernel(const BwdParams p, int row_threads) {
   rmsnorm_backward<kVecs, kSeveral>(p, row_threads);
+}
+
+// Calls of few values: one kernel, in which the first CTAs add up grad_weight
+// straight from grad_y and h (64 channels each, read once more, from L2) while
+// the others do the rows.  No partial sums, no second launch: 517 x 7168 9.2 us
+// instead of 11.3, 256 x 4096 3.9 instead of 6.8.
+constexpr int kWeightCols = 64;
+
+template <int kVecs>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_few_kernel(const BwdParams p, int row_threads,
+                                                                           int weight_ctas) {
+  __shared__ float red[32];
+  __shared__ float sums[32][kWeightCols];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (static_cast<int>(blockIdx.x) < weight_ctas) {
+    // a thread has 8 channels of every (threads / 8)th row; the four rows of a
+    // warp are added, then the warps' sums in their order
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int k = blockIdx.x * kWeightCols + (lane & 7) * 8;
+    float2 acc[4] = {};
+    if (k < p.channels) {
+#pragma unroll 4
+      for (int64_t row = threadIdx.x >> 3; row < p.rows; row += blockDim.x >> 3) {
+        float2 gy[4], h[4];
+        quant::unpack8(*reinterpret_cast<const uint4*>(p.gy + 2 * (at(row, p.ld_gy) + k)), gy);
+        quant::unpack8(*reinterpret_cast<const uint4*>(p.h + 2 * (at(row, p.ld_h) + k)), h);
+        const float r = p.rstd[row];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = __ffma2_rn(gy[i], __fmul2_rn(h[i], make_float2(r, r)), acc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, 8);
+      acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, 8);
+      acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, 16);
+      acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, 16);
+      if (lane < 8) *reinterpret_cast<float2*>(&sums[warp][lane * 8 + 2 * i]) = acc[i];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < kWeightCols; c += blockDim.x) {
+      float s = sums[0][c];
+      for (int i = 1; i < warps; ++i) s += sums[i][c];
+      if (blockIdx.x * kWeightCols + c < p.channels) p.gw[blockIdx.x * kWeightCols + c] = s;
+    }
+    return;
+  }
+  const int t = threadIdx.x % row_threads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x - weight_ctas) * (blockDim.x / row_threads) + threadIdx.x / row_threads;
+  const bool on = row < p.rows;
+  const float rstd = on ? p.rstd[row] : 0.0f;
+  uint4 gv[kVecs], hv[kVecs], rv[kVecs];
+  float dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int k = (t + i * row_threads) * 8;
+    gv[i] = hv[i] = rv[i] = make_uint4(0, 0, 0, 0);
+    if (on && k < p.channels) {
+      gv[i] = *reinterpret_cast<const uint4*>(p.gy + 2 * (at(row, p.ld_gy) + k));
+      hv[i] = *reinterpret_cast<const uint4*>(p.h + 2 * (at(row, p.ld_h) + k));
+      if (p.gh) rv[i] = *reinterpret_cast<const uint4*>(p.gh + 2 * (at(row, p.ld_gh) + k));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int k = (t + i * row_threads) * 8;
+    if (on && k < p.channels) dot += dot8(p, k, gv[i], hv[i]);
+  }
+  dot = row_sum(dot, red, row_threads);
+  const float c = backward_factor(p, rstd, dot);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int k = (t + i * row_threads) * 8;
+    float2 unused[4] = {};
+    if (on && k < p.channels) backward8(p, p.gx + 2 * at(row, p.ld_gx), k, gv[i], hv[i], rv[i], rstd, c, unused);
+  }
 }
 
 // Longer rows: read twice, the sums of grad_y n in memory between rows (a
