@@ -78,6 +78,14 @@ int launch(const void* kernel, dim3 grid, dim3 block, cudaStream_t stream, void*
   return e == cudaSuccess ? SDQ_OK : sdq_internal::cuda_fail(e);
 }
 
+// Whether two bf16 arrays of rows share memory (or lie in each other's gaps).
+bool overlap(const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t rows, int64_t channels) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t na = 2 * static_cast<uintptr_t>((rows - 1) * ld_a + channels);
+  const uintptr_t nb = 2 * static_cast<uintptr_t>((rows - 1) * ld_b + channels);
+  return pa < pb + nb && pb < pa + na;
+}
+
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
 // Threads of a row of `vecs` vectors where several rows share a CTA: 4, 8 or 16
@@ -234,8 +242,11 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
   const int kv_few = vecs <= 512 ? 1 : 2;
   int threads_few = threads_of((vecs + kv_few - 1) / kv_few);
   const int rows_few = std::max(1, 256 / threads_few);
-  // (the CTAs of the weight's gradient take threads / 8 rows at a time)
-  if (vecs <= 2 * sdq::norm::kMaxThreads && rows * channels <= kFewValues && rows <= 2 * threads_few * rows_few) {
+  // (The CTAs of the weight's gradient take threads / 8 rows at a time.  They read
+  // grad_y and h while others write grad_x: not where that is written over them.)
+  const bool over = overlap(grad_x, ld_grad_x, grad_y, ld_grad_y, rows, channels) ||
+                    overlap(grad_x, ld_grad_x, h, ld_h, rows, channels);
+  if (!over && vecs <= 2 * sdq::norm::kMaxThreads && rows * channels <= kFewValues && rows <= 2 * threads_few * rows_few) {
     int weight_ctas = static_cast<int>((channels + sdq::norm::kWeightCols - 1) / sdq::norm::kWeightCols);
     void* args[] = {&p, &threads_few, &weight_ctas};
     return launch(kv_few == 1 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_few_kernel<1>)

@@ -305,6 +305,14 @@ def test_norm_backward_strided_and_in_place():
         _check_bwd(3, 16640, torch.float32, True, 4, pad=16, alias=alias)
 
 
+@pytest.mark.parametrize("rows,channels", [(300, 1040), (500, 256), (200, 7168), (900, 3008)])
+def test_norm_backward_of_few_rows_in_place(rows, channels):
+    """grad_weight is summed from grad_y and h: it must not meet grad_x written over them."""
+    for alias in ("grad_y", "h", "grad_h"):
+        for seed in range(6):
+            _check_bwd(rows, channels, torch.float32, True, seed, alias=alias)
+
+
 def test_norm_backward_empty_and_repeatable():
     w = torch.ones(64, device="cuda")
     x = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda")
