@@ -172,18 +172,18 @@ __device__ __noinline__ GroupScale group_scale_any(uint32_t amax_bits, Divisor v
     r.scale = e4m3_value(r.byte);
     r.unit = __fmul_rn(r.scale, v.g);
     r.inv = __frcp_rn(r.unit);
-    if (!(r.unit > 7.9e-31f && r.unit < 1.2e30f)) r.mode = 1;   // outside 2^+-100
+    // units outside 2^+-100, or quotients past it: no Newton step on those
+    if (!(r.unit > 7.9e-31f && r.unit < 1.2e30f && __fmul_rn(amax, r.inv) < 1.2e30f)) r.mode = 1;
   }
   return r;
 }
 
-// amax_bits: the group's largest magnitude.  Between 2^-90 and 2^90 no step
-// leaves the normal range.
+// amax_bits: the group's largest magnitude.  Between 2^-60 and 2^60, and with a
+// scale per tensor there too, no step leaves the normal range.
 template <Codes C, Scales S>
 __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, const Divisor& v) {
-  constexpr uint32_t kLow = (127u - 90u) << 23, kHigh = (127u + 90u) << 23;
-  // (a scale per tensor may be anything: its units are looked at too)
-  const bool usual = amax_bits - kLow < kHigh - kLow && (S != Scales::kE4M3 || (v.g > 1e-18f && v.g < 1e18f));
+  constexpr uint32_t kLow = (127u - 60u) << 23, kHigh = (127u + 60u) << 23;
+  const bool usual = amax_bits - kLow < kHigh - kLow && (S != Scales::kE4M3 || (v.g > 8.7e-19f && v.g < 1.15e18f));
   if (!usual) return group_scale_any<C, S>(amax_bits, v);
   GroupScale r;
   r.byte = 0;

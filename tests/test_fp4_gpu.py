@@ -88,6 +88,14 @@ def test_quantize_any_global_scale():
         _check(x, "e4m3", "both", torch.tensor([g], device="cuda"), f"g = {g}")
 
 
+def test_quantize_values_and_global_scales_far_apart():
+    """Group maxima over the global scale that overflow or vanish: the scale saturates at 448 or is 2^-9."""
+    for top in (1e-38, 1e-27, 1e-19, 1e-17, 1e15, 1e17, 1e19, 1e25, 3e38):
+        x = torch.cat([(_x(5, 40, 64).float().clamp(-30, 30) / 32 * top * f) for f in (1, 1e-3, 0.04)]).bfloat16()
+        for g in (1e-37, 1e-25, 1e-18, 1.2e-18, 1e-15, 1.0, 1e15, 1.1e18, 1e20, 1e37):
+            _check(x, "e4m3", "both", torch.tensor([g], device="cuda"), f"values to {top}, g = {g}")
+
+
 @pytest.mark.parametrize("scales", ["e8m0", "e4m3"])
 def test_quantize_ties_and_range_ends(scales):
     """Every tie of the codes at several scales, the largest and the smallest bf16 numbers, zeros of both signs."""
