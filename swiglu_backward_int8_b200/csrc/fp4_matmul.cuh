@@ -395,46 +395,48 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     fence_before();
-    if (ranks > 1) {   // (after a wait that ran out the sums are of no use, as the status says)
-      __syncwarp();
-      cluster_arrive();
-      cluster_wait();
-      if (b0 + row < p.rows_b) {
-        const int first = rank * p.share, last = min(first + p.share, cols);
-        Column out(p, a0 + first, b0 + row);
-        for (int c = first; c < last; c += 4) {
-          float4 v = load_shared4(slot(0, row, (c - first) >> 2));
-#pragma unroll
-          for (int r = 1; r < 8; ++r) {
-            if (r < ranks) {
-              const float4 u = load_shared4(slot(r, row, (c - first) >> 2));
-              v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-            }
-          }
-          const float s[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < last) out.put(s[e] * alpha);
-        }
-      }
-    }
   }
   if (warp < 2 && ranks > 1) {   // the barriers count every thread
     __syncwarp();
     cluster_wait();
-    cluster_arrive();
-    cluster_wait();
-  }
-  __syncthreads();
-  if (threadIdx.x == 0 && abort_flag) {   // copies still in flight write this CTA's shared memory
-    for (int i = max(0, issued_flag - p.stages); i < issued_flag; ++i)
-      mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1, sync.limit_ns);
   }
   __syncthreads();
   __syncwarp();
+  // Tensor memory goes back before the CTA waits for others: a CTA of theirs may
+  // be waiting for it, behind another kernel that waits for this one.
   if (warp == 1) {
     fence_after();
     tmem_free(tmem, Z::kCols);
+  }
+  if (ranks > 1) {   // (after a wait that ran out the sums are of no use, as the status says)
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    const int row = (warp & 3) * 32 + lane;
+    if (warp >= 2 && b0 + row < p.rows_b) {
+      const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f);
+      const int cols = static_cast<int>(min(static_cast<int64_t>(p.cols), p.rows_a - a0));
+      const int first = rank * p.share, last = min(first + p.share, cols);
+      Column out(p, a0 + first, b0 + row);
+      for (int c = first; c < last; c += 4) {
+        float4 v = load_shared4(slot(0, row, (c - first) >> 2));
+#pragma unroll
+        for (int r = 1; r < 8; ++r) {
+          if (r < ranks) {
+            const float4 u = load_shared4(slot(r, row, (c - first) >> 2));
+            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+          }
+        }
+        const float s[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < last) out.put(s[e] * alpha);
+      }
+    }
+  }
+  if (threadIdx.x == 0 && abort_flag) {   // copies still in flight write this CTA's shared memory
+    for (int i = max(0, issued_flag - p.stages); i < issued_flag; ++i)
+      mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1, sync.limit_ns);
   }
 }
 

@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t acc = tmem + (k > 0 && (k & 1) ? Z::kAcc1 : 0) + lanes;
       const int start = (k & 1) == 0 ? Z::kAcc1 / 64 : 0;
       if (k >= 0 && half >= Z::kShared / 64) {   // none of its pieces is shared: it is done with the tile before
+        fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(freed0 + 8 * (k & 1));
       }
