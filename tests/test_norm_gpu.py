@@ -299,6 +299,20 @@ def test_norm_backward(rows, channels, with_gh):
     _check_bwd(rows, channels, torch.bfloat16 if with_gh else torch.float32, with_gh, rows + channels)
 
 
+@pytest.mark.parametrize("codes,scales,group", [("int8", "fp32", 128), ("e4m3", "fp32", 0), ("e2m1", "e8m0", 32)])
+@pytest.mark.parametrize("rows,channels", [(2601, 1408), (1199, 2400), (1502, 2816), (1203, 3584)])
+def test_norm_rows_of_odd_warps(codes, scales, group, rows, channels):
+    """Three, five, six and seven warps a row, several rows a CTA and several rounds, the last not whole."""
+    gen = torch.Generator(device="cuda").manual_seed(rows + channels)
+    _run(_rows(gen, rows, channels, 1.0), torch.rand(channels, generator=gen, device="cuda") - 0.5,
+         _rows(gen, rows, channels, 1.0), codes, scales, group)
+
+
+@pytest.mark.parametrize("rows,channels", [(3001, 1408), (5003, 1536)])
+def test_norm_backward_rows_of_odd_warps(rows, channels):
+    _check_bwd(rows, channels, torch.bfloat16, True, rows + channels)
+
+
 def test_norm_backward_strided_and_in_place():
     for alias in ("grad_y", "h", "grad_h"):
         _check_bwd(40, 528, torch.float32, True, 3, pad=16, alias=alias)
