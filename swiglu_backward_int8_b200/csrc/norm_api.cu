@@ -269,9 +269,11 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
                   dim3(static_cast<unsigned>(weight_ctas + (rows + rows_few - 1) / rows_few)),
                   dim3(threads_few * rows_few), s, args);
   }
-  // Vectors a thread, and rows a CTA: several short ones.
-  const int kv = vecs <= 16 ? 1 : vecs <= 1024 ? 2 : vecs <= 2048 ? 4 : 0;
-  const bool several = vecs <= 256;
+  // Vectors a thread: two, or four where two leave a multiprocessor one CTA (8192 x
+  // 8192: 103 us with two, 98 with four; 16384 x 4096: 92 and 96).  Rows a CTA:
+  // several of up to six warps (16384 x 2400, five: 72 us alone, 65 four together).
+  const int kv = vecs <= 16 ? 1 : vecs <= 768 ? 2 : vecs <= 2048 ? 4 : 0;
+  const bool several = vecs <= 384;
   int row_threads = several ? threads_of((vecs + kv - 1) / kv) : kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
   const int rows_cta = several ? rows_of(row_threads, 256) : 1;
   const int threads = row_threads * rows_cta;
@@ -283,7 +285,7 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
                   : several ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<2, true>)
                   : kv == 2 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<2, false>)
                             : reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<4, false>);
-  // at most 16 channels a thread, of at most 384 threads: 24 KB
+  // at most 16 channels a thread, of at most 640 threads: 40 KB
   const size_t smem = rows_cta > 1 ? static_cast<size_t>(rows_cta) * channels * 4 : 0;
   void* args[] = {&p, &row_threads};
   if (const int e = launch(k, dim3(p.parts), dim3(threads), s, args, smem)) return e;

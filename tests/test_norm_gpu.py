@@ -308,7 +308,8 @@ def test_norm_rows_of_odd_warps(codes, scales, group, rows, channels):
          _rows(gen, rows, channels, 1.0), codes, scales, group)
 
 
-@pytest.mark.parametrize("rows,channels", [(3001, 1408), (5003, 1536)])
+@pytest.mark.parametrize("rows,channels", [(3001, 1408), (5003, 1536), (1303, 2400), (1502, 2816), (1201, 3584),
+                                           (700, 6144), (650, 6160)])
 def test_norm_backward_rows_of_odd_warps(rows, channels):
     _check_bwd(rows, channels, torch.bfloat16, True, rows + channels)
 
