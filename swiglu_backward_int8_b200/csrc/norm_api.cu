@@ -92,26 +92,13 @@ int round_up(int v, int m) { return (v + m - 1) / m * m; }
 // lanes, or whole warps.
 int threads_of(int vecs) { return vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : round_up(vecs, 32); }
 
-// Rows that share a CTA of about `target` threads: as many as make its warps a
-// multiple of four, which the quarters of a multiprocessor share evenly (norm of
-// 4099 x 1408, three warps a row: 9.2 us with one row a CTA, 8.2 with four), but
-// not in CTAs of more than 20 warps, one of which is too much of a multiprocessor
-// (2000 x 3584, seven warps: 11.6 us with one row, 13.0 with four).  The backward of
-// 16384 x 1408: 47.3 us with two rows a CTA, 40.3 with four.
-int rows_of(int row_threads, int target) {
-  if (row_threads < 32) return target / row_threads;
-  const int warps = row_threads / 32;
-  int rows = warps % 4 == 0 ? 1 : warps % 2 == 0 ? 2 : 4;
-  if (rows * row_threads > 640) return 1;
-  while (2 * rows * row_threads <= target) rows *= 2;
-  return rows;
-}
-
-// CTAs of `threads` threads with `regs` registers each that a multiprocessor
-// holds: each quarter of it has 16384 registers and takes every fourth warp.
+// CTAs of `threads` threads with `regs` registers each that a multiprocessor's
+// 65536 registers hold.  (A grid that leaves room for more is the worse also
+// because the next kernel's CTAs, which wait there, then spread unevenly: 16384 x
+// 1408, three warps a row, ten CTAs: 25.1 us a call in a row of them, with eight
+// 30.3.)
 int ctas_per_sm(int threads, int regs) {
-  const int warps = 16384 / (32 * regs), each = (threads / 32 + 3) / 4;
-  return std::max(1, std::min(warps / each, 2048 / threads));
+  return std::max(1, std::min(65536 / (threads * regs), 2048 / threads));
 }
 
 }  // namespace
@@ -187,7 +174,7 @@ int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t
   // the next row loaded ahead.  Rows that no CTA holds: read again.
   const Variant v = vecs > sdq::norm::kMaxThreads ? Variant::kLong : rows <= sms ? Variant::kFew : Variant::kMany;
   int row_threads = v == Variant::kLong ? sdq::norm::kMaxThreads : v == Variant::kMany ? threads_of(vecs) : round_up(vecs, 32);
-  const int rows_cta = v == Variant::kMany ? rows_of(row_threads, 128) : 1;
+  const int rows_cta = v == Variant::kMany ? std::max(1, 128 / row_threads) : 1;
   int64_t grid = (rows + rows_cta - 1) / rows_cta;
   if (v == Variant::kMany)
     grid = std::min<int64_t>(grid, int64_t{sms} * ctas_per_sm(row_threads * rows_cta, sdq::norm::kAheadRegs));
@@ -270,12 +257,12 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
                   dim3(threads_few * rows_few), s, args);
   }
   // Vectors a thread: two, or four where two leave a multiprocessor one CTA (8192 x
-  // 8192: 103 us with two, 98 with four; 16384 x 4096: 92 and 96).  Rows a CTA:
-  // several of up to six warps (16384 x 2400, five: 72 us alone, 65 four together).
+  // 8192: 103 us with two, 99 with four; 16384 x 4096: 92 and 96).  Rows a CTA:
+  // several short ones.
   const int kv = vecs <= 16 ? 1 : vecs <= 768 ? 2 : vecs <= 2048 ? 4 : 0;
-  const bool several = vecs <= 384;
+  const bool several = vecs <= 256;
   int row_threads = several ? threads_of((vecs + kv - 1) / kv) : kv ? round_up((vecs + kv - 1) / kv, 32) : sdq::norm::kMaxThreads;
-  const int rows_cta = several ? rows_of(row_threads, 256) : 1;
+  const int rows_cta = several ? std::max(1, 256 / row_threads) : 1;
   const int threads = row_threads * rows_cta;
   const int per_sm = kv ? std::min(4, ctas_per_sm(threads, sdq::norm::backward_regs(kv))) : 1;
   p.parts = static_cast<int32_t>(
@@ -285,7 +272,7 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
                   : several ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<2, true>)
                   : kv == 2 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<2, false>)
                             : reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_kernel<4, false>);
-  // at most 16 channels a thread, of at most 640 threads: 40 KB
+  // at most 256 / row_threads rows of 16 row_threads channels: 16 KB
   const size_t smem = rows_cta > 1 ? static_cast<size_t>(rows_cta) * channels * 4 : 0;
   void* args[] = {&p, &row_threads};
   if (const int e = launch(k, dim3(p.parts), dim3(threads), s, args, smem)) return e;

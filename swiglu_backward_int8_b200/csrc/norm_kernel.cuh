@@ -16,7 +16,7 @@
 // warp or a CTA); longer rows are read again from L2.  DRAM bounds long calls:
 // 16384 x 7168, residual, E4M3 codes, one scale for 128 channels, 137 us, 92 % of
 // the measured copy's rate; the backward of 16384 x 4096, 92 us, 89 %, of 16384 x
-// 7168, 190 us, 76 % (14 warps a multiprocessor, by registers).  Short calls are
+// 7168, 176 us, 82 % (14 warps a multiprocessor, by registers).  Short calls are
 // bound by the row's latency (load, sum over the CTA, scale, store) and the
 // launch: 1 x 7168, 2.9 us; the backward of 517 x 7168, 9.2 us.
 #pragma once
