@@ -92,13 +92,14 @@ int round_up(int v, int m) { return (v + m - 1) / m * m; }
 // lanes, or whole warps.
 int threads_of(int vecs) { return vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : round_up(vecs, 32); }
 
-// CTAs of `threads` threads with `regs` registers each that a multiprocessor's
-// 65536 registers hold.  (A grid that leaves room for more is the worse also
-// because the next kernel's CTAs, which wait there, then spread unevenly: 16384 x
-// 1408, three warps a row, ten CTAs: 25.1 us a call in a row of them, with eight
-// 30.3.)
+// CTAs of `threads` threads with `regs` registers each that a multiprocessor
+// holds: each quarter of it has 16384 registers.  (A grid that leaves room for more
+// is the worse also because the next kernel's CTAs, which wait there, then spread
+// unevenly: 16384 x 1408, three warps a row, ten CTAs: 25.1 us a call in a row of
+// them, with eight 30.3.)
 int ctas_per_sm(int threads, int regs) {
-  return std::max(1, std::min(65536 / (threads * regs), 2048 / threads));
+  const int warps = 4 * (16384 / (32 * regs));
+  return std::max(1, std::min(warps / (threads / 32), 2048 / threads));
 }
 
 }  // namespace
@@ -243,12 +244,16 @@ int sdq_rmsnorm_backward(const void* grad_y, int64_t ld_grad_y, const void* h, i
   const int vecs = static_cast<int>((channels + 7) / 8);
   const int kv_few = vecs <= 512 ? 1 : 2;
   int threads_few = threads_of((vecs + kv_few - 1) / kv_few);
-  const int rows_few = std::max(1, 256 / threads_few);
-  // (The CTAs of the weight's gradient take threads / 8 rows at a time.  They read
-  // grad_y and h while others write grad_x: not where that is written over them.)
+  // CTAs of up to 1024 threads for short rows (900 x 2048: 6.7 us, 8.8 with 512
+  // threads; 512 x 4096: 6.4 and 8.5 with two rows a CTA): the weight's gradient
+  // takes threads / 8 rows at a time, and is what takes longest where rows are
+  // short.  More of them are left to the kernel below (2000 x 256: 6.8 us, 4.7 there).
+  // (Weight's CTAs read grad_y and h while others write grad_x: not where that is
+  // written over them.)
+  const int rows_few = vecs <= 384 ? std::max(1, 1024 / threads_few) : 1;
   const bool over = overlap(grad_x, ld_grad_x, grad_y, ld_grad_y, rows, channels) ||
                     overlap(grad_x, ld_grad_x, h, ld_h, rows, channels);
-  if (!over && vecs <= 2 * sdq::norm::kMaxThreads && rows * channels <= kFewValues && rows <= 2 * threads_few * rows_few) {
+  if (!over && vecs <= 2 * sdq::norm::kMaxThreads && rows * channels <= kFewValues && rows <= 600 + 8 * vecs) {
     int weight_ctas = static_cast<int>((channels + sdq::norm::kWeightCols - 1) / sdq::norm::kWeightCols);
     void* args[] = {&p, &threads_few, &weight_ctas};
     return launch(kv_few == 1 ? reinterpret_cast<const void*>(sdq::norm::rmsnorm_backward_few_kernel<1>)

@@ -302,7 +302,7 @@ def test_norm_backward(rows, channels, with_gh):
 @pytest.mark.parametrize("codes,scales,group", [("int8", "fp32", 128), ("e4m3", "fp32", 0), ("e2m1", "e8m0", 32)])
 @pytest.mark.parametrize("rows,channels", [(2601, 1408), (1199, 2400), (1502, 2816), (1203, 3584)])
 def test_norm_rows_of_odd_warps(codes, scales, group, rows, channels):
-    """Three, five, six and seven warps a row, several rows a CTA and several rounds, the last not whole."""
+    """Three, five, six and seven warps a row, several rounds of them, the last not whole."""
     gen = torch.Generator(device="cuda").manual_seed(rows + channels)
     _run(_rows(gen, rows, channels, 1.0), torch.rand(channels, generator=gen, device="cuda") - 0.5,
          _rows(gen, rows, channels, 1.0), codes, scales, group)
@@ -312,6 +312,11 @@ def test_norm_rows_of_odd_warps(codes, scales, group, rows, channels):
                                            (700, 6144), (650, 6160)])
 def test_norm_backward_rows_of_odd_warps(rows, channels):
     _check_bwd(rows, channels, torch.bfloat16, True, rows + channels)
+
+
+@pytest.mark.parametrize("rows,channels", [(2003, 2048), (1131, 528), (607, 16), (830, 2832), (1100, 3600), (31, 96)])
+def test_norm_backward_of_few_rows_in_wide_ctas(rows, channels):
+    _check_bwd(rows, channels, torch.float32, True, rows + channels)
 
 
 def test_norm_backward_strided_and_in_place():
