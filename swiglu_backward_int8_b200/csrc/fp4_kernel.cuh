@@ -11,9 +11,9 @@
 //
 // 2 bytes are read and 0.53 or 0.56 written a value and axis.  Along the rows DRAM
 // bounds it (8192 x 4096: 15 to 17 us, 77 to 85 % of the measured copy's rate);
-// along both axes instructions do, 18 a value (28 us, 57 %): the issue slots are
-// 62 % taken, the half-rate integer pipe, which unpacks, converts and compares,
-// nearly full.  Reading back: 15.3 us, 85 %.
+// along both axes instructions do (E8M0 scales 22.4 us, 72 %; E4M3 scales, twice
+// the groups and a Newton step a quotient, 26.7, 61 %): the half-rate integer pipe
+// unpacks, converts and compares.  Reading back: 15.3 us, 85 %.
 #pragma once
 
 #include <cstdint>
@@ -108,14 +108,17 @@ __global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const
       quant::unpack8(vb[i], z);
       uint32_t m = max(quant::amax(y), quant::amax(z));
       if (G == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      const quant::GroupScale gs = quant::group_scale<Codes::kE2M1, S>(m, d);
-      if (i * kStep < rows_here)
-        *reinterpret_cast<uint2*>(q) =
-            make_uint2(quant::codes8<Codes::kE2M1, S>(y, gs).x, quant::codes8<Codes::kE2M1, S>(z, gs).x);
+      uint32_t byte;
+      uint2 codes;
+      quant::with_scale<Codes::kE2M1, S>(m, d, [&](const quant::GroupScale& gs) {
+        byte = gs.byte;
+        codes = make_uint2(quant::codes8<Codes::kE2M1, S>(y, gs).x, quant::codes8<Codes::kE2M1, S>(z, gs).x);
+      });
+      if (i * kStep < rows_here) *reinterpret_cast<uint2*>(q) = codes;
       q += kStep * p.ld_q;
       const int grp = c16 / G;
       if ((c16 & (G - 1)) == 0)
-        sc[(grp >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (grp & 3)] = static_cast<uint8_t>(c16 < nch ? gs.byte : 0u);
+        sc[(grp >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (grp & 3)] = static_cast<uint8_t>(c16 < nch ? byte : 0u);
     }
   }
   __syncthreads();
@@ -135,21 +138,23 @@ __global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const
         ma = quant::amax3(ma, bf16_lo(v[e]), bf16_lo(v[e + 1]));
         mb = quant::amax3(mb, bf16_hi(v[e]), bf16_hi(v[e + 1]));
       }
-      const quant::GroupScale ga = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(ma), d);
-      const quant::GroupScale gb = quant::group_scale<Codes::kE2M1, S>(__float_as_uint(mb), d);
+      uint32_t byte[2];
       const bool in = m0 + grp * G < p.rows_padded;      // whole groups: rows_padded is a multiple of 32
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t q[G / 8];
+        quant::with_scale<Codes::kE2M1, S>(__float_as_uint(h ? mb : ma), d, [&](const quant::GroupScale& gs) {
+          byte[h] = gs.byte;
 #pragma unroll
-        for (int w = 0; w < G / 8; ++w) {
-          float2 y[4];
+          for (int w = 0; w < G / 8; ++w) {
+            float2 y[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y[e] = h ? make_float2(bf16_hi(v[w * 8 + 2 * e]), bf16_hi(v[w * 8 + 2 * e + 1]))
-                     : make_float2(bf16_lo(v[w * 8 + 2 * e]), bf16_lo(v[w * 8 + 2 * e + 1]));
-          q[w] = quant::codes8<Codes::kE2M1, S>(y, h ? gb : ga).x;
-        }
+            for (int e = 0; e < 4; ++e)
+              y[e] = h ? make_float2(bf16_hi(v[w * 8 + 2 * e]), bf16_hi(v[w * 8 + 2 * e + 1]))
+                       : make_float2(bf16_lo(v[w * 8 + 2 * e]), bf16_lo(v[w * 8 + 2 * e + 1]));
+            q[w] = quant::codes8<Codes::kE2M1, S>(y, gs).x;
+          }
+        });
         uint8_t* o = ct + (c + h) * kCodePitch;
         if constexpr (G == 32)
           *reinterpret_cast<uint4*>(o + ((grp ^ ((c >> 1) & 3)) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
@@ -157,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const
           *reinterpret_cast<uint2*>(o + (((grp >> 1) ^ ((c >> 1) & 3)) << 4) + (grp & 1) * 8) = make_uint2(q[0], q[1]);
       }
       uint8_t* o = sct + (grp >> 2) * 512 + (grp & 3);
-      o[(c & 31) * 16 + (c >> 5) * 4] = static_cast<uint8_t>(in ? ga.byte : 0u);
-      o[((c + 1) & 31) * 16 + (c >> 5) * 4] = static_cast<uint8_t>(in ? gb.byte : 0u);
+      o[(c & 31) * 16 + (c >> 5) * 4] = static_cast<uint8_t>(in ? byte[0] : 0u);
+      o[((c + 1) & 31) * 16 + (c >> 5) * 4] = static_cast<uint8_t>(in ? byte[1] : 0u);
     }
     __syncthreads();
     store_scale_tiles<kAtoms>(sct, p.st + static_cast<int64_t>(tile_k) * p.tiles_m * 512,

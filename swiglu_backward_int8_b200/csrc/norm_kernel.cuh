@@ -14,7 +14,7 @@
 //
 // One pass over the arrays, a row in a CTA's registers (several short rows to a
 // warp or a CTA); longer rows are read again from L2.  DRAM bounds long calls:
-// 16384 x 7168, residual, E4M3 codes, one scale for 128 channels, 137 us, 92 % of
+// 16384 x 7168, residual, E4M3 codes, one scale for 128 channels, 132 us, 95 % of
 // the measured copy's rate; the backward of 16384 x 4096, 92 us, 89 %, of 16384 x
 // 7168, 176 us, 82 % (14 warps a multiprocessor, by registers).  Short calls are
 // bound by the row's latency (load, sum over the CTA, scale, store) and the
@@ -270,12 +270,12 @@ __device__ __forceinline__ void rmsnorm_quant(const Params& p, int row_threads) 
     const bool whole = C != Codes::kE2M1 && p.group == 0;   // one scale a row
     m = whole ? row_max(m, reinterpret_cast<uint32_t*>(red[flip][1]), row_threads) : group_max<C, S>(group, m);
     flip ^= 1;
-    const quant::GroupScale g = quant::group_scale<C, S>(m, d);
-    if (on) {
-      const int32_t begun = whole ? (t == 0 ? 0 : -1) : group_begun<C, S>(p.group, k);
-      if (begun >= 0) store_scale<C, S>(p, row, begun, g);
-      store_codes<C, S>(p, row, k, y, g);
-    }
+    if (on)
+      quant::with_scale<C, S>(m, d, [&](const quant::GroupScale& g) {
+        const int32_t begun = whole ? (t == 0 ? 0 : -1) : group_begun<C, S>(p.group, k);
+        if (begun >= 0) store_scale<C, S>(p, row, begun, g);
+        store_codes<C, S>(p, row, k, y, g);
+      });
     if (row < p.rows) pad_scales<C>(p, row, t);   // (a short row has fewer vectors than groups to pad)
     if (!kAhead) break;   // one row a thread
   }
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(const Params
 }
 
 // 64 registers: eight warps a quarter of a multiprocessor.  (Two vectors a thread
-// and 80 registers, six warps: 160 us for 16384 x 7168 where this takes 138.)
+// and 80 registers, six warps: 160 us for 16384 x 7168 where this took 138.)
 constexpr int kAheadRegs = 64;
 
 template <Codes C, Scales S>

@@ -90,7 +90,11 @@ __device__ __forceinline__ int ceil_exp(float t) {
 }
 
 // One E4M3 byte (round to nearest even, saturated to 448).
-__device__ __forceinline__ uint32_t e4m3_byte(float v) { return e4m3x4(v, 0.0f, 0.0f, 0.0f) & 0xFFu; }
+__device__ __forceinline__ uint32_t e4m3_byte(float v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 b;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %1, %2;\n\tcvt.u32.u16 %0, b;\n}\n" : "=r"(r) : "f"(0.0f), "f"(v));
+  return r;
+}
 
 // The value of an E4M3 byte.
 __device__ __forceinline__ float e4m3_value(uint32_t b) {
@@ -117,16 +121,20 @@ __device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
 }
 
 // What the groups of a call share: the divisor of a group's largest magnitude,
-// its reciprocal, and the scale per tensor.
+// its reciprocal, the scale per tensor, and how far the usual magnitudes reach up
+// from kLowBits, as bits.
 struct Divisor {
   float d, inv, g;
+  uint32_t span;
 };
+constexpr uint32_t kLowBits = (127u - 60u) << 23, kHighBits = (127u + 60u) << 23;
 template <Codes C, Scales S>
 __device__ __forceinline__ Divisor divisor(const float* global) {
   Divisor v;
   v.g = S == Scales::kE4M3 && global ? *global : 1.0f;
   v.d = S == Scales::kE4M3 ? __fmul_rn(6.0f, v.g) : qmax<C>();
   v.inv = S == Scales::kE4M3 ? __frcp_rn(v.d) : 1.0f / qmax<C>();
+  v.span = S != Scales::kE4M3 || (v.g > 8.7e-19f && v.g < 1.15e18f) ? kHighBits - kLowBits : 0u;
   return v;
 }
 
@@ -178,13 +186,12 @@ __device__ __noinline__ GroupScale group_scale_any(uint32_t amax_bits, Divisor v
   return r;
 }
 
-// amax_bits: the group's largest magnitude.  Between 2^-60 and 2^60, and with a
-// scale per tensor there too, no step leaves the normal range.
+// Between 2^-60 and 2^60, and with a scale per tensor there too, no step leaves
+// the normal range.
+__device__ __forceinline__ bool usual(uint32_t amax_bits, const Divisor& v) { return amax_bits - kLowBits < v.span; }
+
 template <Codes C, Scales S>
-__device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, const Divisor& v) {
-  constexpr uint32_t kLow = (127u - 60u) << 23, kHigh = (127u + 60u) << 23;
-  const bool usual = amax_bits - kLow < kHigh - kLow && (S != Scales::kE4M3 || (v.g > 8.7e-19f && v.g < 1.15e18f));
-  if (!usual) return group_scale_any<C, S>(amax_bits, v);
+__device__ __forceinline__ GroupScale group_scale_usual(uint32_t amax_bits, const Divisor& v) {
   GroupScale r;
   r.byte = 0;
   r.mode = 0;
@@ -203,6 +210,23 @@ __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, const Divi
     r.inv = reciprocal(r.unit);
   }
   return r;
+}
+
+// amax_bits: the group's largest magnitude.
+template <Codes C, Scales S>
+__device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits, const Divisor& v) {
+  return usual(amax_bits, v) ? group_scale_usual<C, S>(amax_bits, v) : group_scale_any<C, S>(amax_bits, v);
+}
+
+// f with the scale of a group: the usual scales apart, so that what f does with
+// them asks no more of what kind they are (4-bit codes along both axes, 8192 x 4096,
+// E8M0 scales: 27.1 us with one scale struct for all, 22.4 so).
+template <Codes C, Scales S, class F>
+__device__ __forceinline__ void with_scale(uint32_t amax_bits, const Divisor& d, F f) {
+  if (usual(amax_bits, d))
+    f(group_scale_usual<C, S>(amax_bits, d));
+  else
+    f(group_scale_any<C, S>(amax_bits, d));
 }
 
 // v * inv rounded to whole numbers by one fused multiply-add each (quant_bits).
