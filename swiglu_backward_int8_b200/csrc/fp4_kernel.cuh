@@ -11,8 +11,8 @@
 //
 // 2 bytes are read and 0.53 or 0.56 written a value and axis.  Along the rows DRAM
 // bounds it (8192 x 4096: 15 to 17 us, 77 to 85 % of the measured copy's rate);
-// along both axes instructions do (E8M0 scales 22.4 us, 72 %; E4M3 scales, twice
-// the groups and a Newton step a quotient, 26.7, 61 %): the half-rate integer pipe
+// along both axes instructions do (E8M0 scales 22.2 us, 72 %; E4M3 scales, twice
+// the groups and a Newton step a quotient, 26.3, 62 %): the half-rate integer pipe
 // unpacks, converts and compares.  Reading back: 15.3 us, 85 %.
 #pragma once
 
@@ -57,8 +57,10 @@ __device__ __forceinline__ void store_scale_tiles(const uint8_t* sc, uint8_t* ou
   }
 }
 
+// CTAs a multiprocessor: four, but three where the columns' groups of 32, or both
+// axes, need more registers (both axes, E8M0 scales: 22 us with three, 29 with four).
 template <Scales S, bool kRows, bool kCols>
-__global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, kCols && (kRows || S == Scales::kE8M0) ? 3 : 4) quantize_kernel(const QuantParams p) {
   constexpr int G = S == Scales::kE8M0 ? 32 : 16;
   constexpr int kGroups = kTile / G;          // groups of a tile along either axis
   constexpr int kAtoms = kGroups / 4;         // scale tiles of a tile
@@ -106,7 +108,8 @@ __global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const
       float2 y[4], z[4];
       quant::unpack8(va[i], y);
       quant::unpack8(vb[i], z);
-      uint32_t m = max(quant::amax(y), quant::amax(z));
+      uint32_t m = quant::amax_bf16x2(quant::amax_bf16x2(va[i]), quant::amax_bf16x2(vb[i]));
+      m = max(quant::magnitude_lo(m), quant::magnitude_hi(m));
       if (G == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       uint32_t byte;
       uint2 codes;
@@ -130,20 +133,21 @@ __global__ void __launch_bounds__(kThreads, kCols ? 3 : 4) quantize_kernel(const
     for (int i = 0; i < kGroups / 4; ++i) {
       const int grp = (t >> 6) + 4 * i;         // the group of rows
       uint32_t v[G];
-      float ma = 0.0f, mb = 0.0f;
+      uint32_t m = 0, n = 0;
 #pragma unroll
       for (int e = 0; e < G; ++e) v[e] = *reinterpret_cast<const uint32_t*>(tile + (grp * G + e) * kPitch + c * 2);
 #pragma unroll
       for (int e = 0; e < G; e += 2) {
-        ma = quant::amax3(ma, bf16_lo(v[e]), bf16_lo(v[e + 1]));
-        mb = quant::amax3(mb, bf16_hi(v[e]), bf16_hi(v[e + 1]));
+        m = quant::amax_bf16x2(m, v[e]);
+        n = quant::amax_bf16x2(n, v[e + 1]);
       }
+      m = quant::amax_bf16x2(m, n);
       uint32_t byte[2];
       const bool in = m0 + grp * G < p.rows_padded;      // whole groups: rows_padded is a multiple of 32
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t q[G / 8];
-        quant::with_scale<Codes::kE2M1, S>(__float_as_uint(h ? mb : ma), d, [&](const quant::GroupScale& gs) {
+        quant::with_scale<Codes::kE2M1, S>(h ? quant::magnitude_hi(m) : quant::magnitude_lo(m), d, [&](const quant::GroupScale& gs) {
           byte[h] = gs.byte;
 #pragma unroll
           for (int w = 0; w < G / 8; ++w) {

@@ -53,6 +53,20 @@ __device__ __forceinline__ uint32_t amax(const float2 (&y)[kPairs]) {
   return __float_as_uint(m);
 }
 
+// The larger magnitudes of two pairs of bf16 numbers, with signs of their own; a
+// NaN where one is.
+__device__ __forceinline__ uint32_t amax_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t amax_bf16x2(const uint4& v) {
+  return amax_bf16x2(amax_bf16x2(v.x, v.y), amax_bf16x2(v.z, v.w));
+}
+// One number of a pair without its sign, as the bits of an fp32 number.
+__device__ __forceinline__ uint32_t magnitude_lo(uint32_t v) { return (v << 16) & 0x7FFF0000u; }
+__device__ __forceinline__ uint32_t magnitude_hi(uint32_t v) { return v & 0x7FFF0000u; }
+
 __device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

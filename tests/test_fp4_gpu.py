@@ -134,6 +134,26 @@ def test_quantize_strided():
     assert (q[:, 80:] == 0x77).all() and (qt[:, 32:] == 0x77).all()
 
 
+@pytest.mark.parametrize("scales,n", [("e8m0", 32), ("e4m3", 16)])
+def test_quantize_non_finite_values_in_every_place_of_a_group(scales, n):
+    """Along both axes a group reads back as NaN where it holds a NaN or an infinity of either sign, nowhere else."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.randn(256, 224, generator=gen, device="cuda").bfloat16()
+    bits = x.view(torch.int16)
+    for i, b in enumerate((0x7FC0, -0x40, 0x7F80, -0x80, 0x7F81, -1)):       # NaN, infinity, NaN of other bits
+        k = torch.arange(i, 224, 41 + i, device="cuda")
+        bits[(k * 7 + 29 * i) % 256, k] = b
+    bad = ~x.isfinite()
+    q, s, qt, st = sdq.quantize_fp4(x, scales, "both")
+    want = bad.view(256, -1, n).any(2).repeat_interleave(n, 1)
+    assert torch.equal(sdq.dequantize_fp4(q, s).isnan(), want)
+    want = bad.t().reshape(224, -1, n).any(2).repeat_interleave(n, 1)
+    assert torch.equal(sdq.dequantize_fp4(qt, st).isnan(), want)
+    for axis, pair in (("rows", (q, s)), ("columns", (qt, st))):
+        got = sdq.quantize_fp4(x, scales, axis)
+        assert torch.equal(sdq.dequantize_fp4(*got).isnan(), sdq.dequantize_fp4(*pair).isnan())
+
+
 @pytest.mark.parametrize("scales", ["e8m0", "e4m3"])
 @pytest.mark.parametrize("rows,k", [(1, 32), (129, 96), (200, 2080)])
 def test_dequantize_every_code_and_scale(scales, rows, k):
