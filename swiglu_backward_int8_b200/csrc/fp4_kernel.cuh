@@ -12,8 +12,9 @@
 // 2 bytes are read and 0.53 or 0.56 written a value and axis.  Along the rows DRAM
 // bounds it (8192 x 4096: 15 to 17 us, 77 to 85 % of the measured copy's rate);
 // along both axes instructions do (E8M0 scales 22.2 us, 72 %; E4M3 scales, twice
-// the groups and a Newton step a quotient, 26.3, 62 %): the half-rate integer pipe
-// unpacks, converts and compares.  Reading back: 15.3 us, 85 %.
+// the groups and a Newton step a quotient, 26.3, 62 %): 16 a value, 59 % of the issue
+// slots by 24 warps, half of them in the half-rate integer pipe, which unpacks,
+// converts and compares.  Reading back: 15.3 us, 85 %.
 #pragma once
 
 #include <cstdint>
