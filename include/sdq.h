@@ -303,7 +303,8 @@ int sdq_validate_swiglu_q8_1(const void* gate, int64_t ld_gate, const void* up, 
  *                        positive; a NULL pointer: 1); a code of 1 stands for
  *                        fl32(scale * g); code = round-to-nearest-even of the
  *                        quotient, saturated to +-6.  A g of amax(tensor) / 2688
- *                        uses the whole range of the scales.
+ *                        uses the whole range of the scales (0 for a tensor of
+ *                        zeros, whose groups are those of the next line).
  *   an all-zero group    scale 1, codes 0 (E4M3 and E2M1 zeros keep their sign)
  *   a group holding a NaN or an infinity: scale NaN (fp32 NaN, E8M0 0xFF, E4M3
  *                        0x7F), codes 0: all of the group reads back as NaN

@@ -188,8 +188,11 @@ __device__ __noinline__ GroupScale group_scale_any(uint32_t amax_bits, Divisor v
     r.byte = static_cast<uint32_t>(k + 127);
     r.scale = r.unit = exp2i(k);
     r.inv = exp2i(-k);                          // both exact: no rounding before the code's
+  } else if (amax_bits == 0) {                  // whatever the scale per tensor: it is 0 where all of the tensor is
+    r.byte = 0x38u;
+    r.scale = r.unit = r.inv = 1.0f;
   } else {
-    r.byte = amax_bits ? e4m3_byte(__fdiv_rn(amax, v.d)) : 0x38u;
+    r.byte = e4m3_byte(__fdiv_rn(amax, v.d));
     if (r.byte == 0) r.byte = 1;                // 2^-9: a group this small still has codes
     r.scale = e4m3_value(r.byte);
     r.unit = __fmul_rn(r.scale, v.g);

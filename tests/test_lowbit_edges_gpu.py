@@ -1,0 +1,54 @@
+"""The norm, its backward, the 4-bit quantizer and the product at the ends of their ranges: tensors of zeros with
+the scale per tensor that zeros give, rows and scales whose squares and products leave fp32's range."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import swiglu_backward_int8_b200 as sdq
+from tests import lowbit_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def _bytes(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+@pytest.mark.parametrize("rows,channels", [(1, 32), (40, 64), (130, 288)])
+def test_tensor_of_zeros_with_its_own_scale_per_tensor(rows, channels):
+    """amax / 2688 of zeros is 0: scales of 1 and codes of 0, which keep their sign, along both axes and after a norm."""
+    x = torch.zeros(rows, channels, dtype=torch.bfloat16, device="cuda")
+    x[:, 1::2] = -0.0
+    g = (x.float().abs().amax() / 2688).reshape(1)
+    assert float(g) == 0
+    pad = -(-rows // 32) * 32
+    s, st = (torch.full(sdq.fp4_scale_shape(r, k, "e4m3"), 0xA5, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+             for r, k in ((rows, channels), (channels, pad)))
+    q, _, qt, _ = sdq.quantize_fp4(x, "e4m3", "both", s=s, s_t=st, global_scale=g)
+    assert (R.unpack(_bytes(q)) == np.where(np.arange(channels) % 2, 8, 0)).all()
+    assert (R.unpack(_bytes(qt))[:, :rows] == np.where(np.arange(channels) % 2, 8, 0)[:, None]).all()
+    assert (R.unpack(_bytes(qt))[:, rows:] == 0).all()
+    assert (_bytes(s).reshape(-1)[R.tile_index(rows, channels // 16)] == 0x38).all()
+    assert (_bytes(st).reshape(-1)[R.tile_index(channels, pad // 16)] == 0x38).all()
+    assert (sdq.dequantize_fp4(q, s, g) == 0).all() and (sdq.dequantize_fp4(qt, st, g) == 0).all()
+    q, s, _ = sdq.rmsnorm_quant(x, torch.ones(channels, device="cuda"), codes="e2m1", scales="e4m3", global_scale=g)
+    assert (R.unpack(_bytes(q)) & 7 == 0).all()
+    assert (_bytes(s).reshape(-1)[R.tile_index(rows, channels // 16)] == 0x38).all()
+    y = sdq.matmul_fp4(q, s, q, s, a_global=g, b_global=g)
+    assert (y == 0).all()
+
+
+@pytest.mark.parametrize("g", [1e-45, 1e-38, 0.37, 1e30, 3e38])
+def test_groups_of_zeros_among_others(g):
+    """Rows of zeros next to others, with scales per tensor from the smallest to the largest."""
+    x = torch.randn(70, 96, device="cuda").bfloat16()
+    x[5], x[33:64], x[:, 32:64] = 0, 0, 0
+    q, s, qt, st = sdq.quantize_fp4(x, "e4m3", "both", global_scale=torch.tensor([g], device="cuda"))
+    zero = x == 0
+    for c, t, z in ((q, s, zero), (qt, st, torch.nn.functional.pad(zero.t(), (0, 26), value=True))):
+        c, z = R.unpack(_bytes(c)), z.cpu().numpy()
+        assert (c[z] & 7 == 0).all()
+        none = z.reshape(z.shape[0], -1, 16).all(2)
+        assert none.any() and (_bytes(t).reshape(-1)[R.tile_index(*none.shape)][none] == 0x38).all()
