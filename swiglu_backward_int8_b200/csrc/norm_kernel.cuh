@@ -380,10 +380,11 @@ __device__ __forceinline__ void load_weight8(const uint8_t* weight, int f32, int
   }
 }
 
-// grad_x of eight channels, grad_y n of them added to acc.  c: rstd^3 times the
-// row's mean of grad_y w h.
+// grad_x of eight channels, grad_y n of them added to acc.  mean: the row's mean of
+// grad_y w n.  (In the formula's own order: rstd^3, which would save forming n
+// first, leaves fp32's range while the result is well inside.)
 __device__ __forceinline__ void backward8(const BwdParams& p, uint8_t* gx, int32_t k, const uint4& gyv, const uint4& hv,
-                                          const uint4& ghv, float rstd, float c, float2 (&acc)[4]) {
+                                          const uint4& ghv, float rstd, float mean, float2 (&acc)[4]) {
   float2 gy[4], h[4], gh[4], w[4];
   quant::unpack8(gyv, gy);
   quant::unpack8(hv, h);
@@ -392,9 +393,10 @@ __device__ __forceinline__ void backward8(const BwdParams& p, uint8_t* gx, int32
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 r = make_float2(rstd, rstd);
-    const float2 o = __ffma2_rn(__fmul2_rn(gy[i], w[i]), r, gh[i]);
-    gh[i] = __ffma2_rn(h[i], make_float2(-c, -c), o);
-    acc[i] = __ffma2_rn(gy[i], __fmul2_rn(h[i], r), acc[i]);
+    const float2 n = __fmul2_rn(h[i], r);
+    const float2 d = __ffma2_rn(n, make_float2(-mean, -mean), __fmul2_rn(gy[i], w[i]));
+    gh[i] = __ffma2_rn(d, r, gh[i]);
+    acc[i] = __ffma2_rn(gy[i], n, acc[i]);
   }
   *reinterpret_cast<uint4*>(gx + 2 * k) = quant::pack8(gh);
 }
@@ -409,9 +411,9 @@ __device__ __forceinline__ float dot8(const BwdParams& p, int32_t k, const uint4
   return s.x + s.y;
 }
 
-// rstd^3 mean(grad_y w h), from the row's sum.
-__device__ __forceinline__ float backward_factor(const BwdParams& p, float rstd, float dot) {
-  return rstd * rstd * (rstd * (dot * p.inv_channels));
+// mean(grad_y w n), from the row's sum of grad_y w h.
+__device__ __forceinline__ float backward_mean(const BwdParams& p, float rstd, float dot) {
+  return rstd * (dot * p.inv_channels);
 }
 
 // Rows that fit the registers, kVecs vectors a thread: grad_y and h of the next
@@ -468,11 +470,11 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads
     load(row + stride);
     dot = row_sum(dot, red[flip], row_threads);
     flip ^= 1;
-    const float c = backward_factor(p, rstd, dot);
+    const float mean = backward_mean(p, rstd, dot);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int k = (t + i * row_threads) * 8;
-      if (on && k < p.channels) backward8(p, gx, k, gv[i], hv[i], rv[i], rstd, c, acc[i]);
+      if (on && k < p.channels) backward8(p, gx, k, gv[i], hv[i], rv[i], rstd, mean, acc[i]);
     }
   }
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
@@ -572,12 +574,12 @@ __global__ void __maxnreg__(kVecs == 1 ? 40 : 64) rmsnorm_backward_few_kernel(co
     if (on && k < p.channels) dot += dot8(p, k, gv[i], hv[i]);
   }
   dot = row_sum(dot, red, row_threads);
-  const float c = backward_factor(p, rstd, dot);
+  const float mean = backward_mean(p, rstd, dot);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int k = (t + i * row_threads) * 8;
     float2 unused[4] = {};
-    if (on && k < p.channels) backward8(p, p.gx + 2 * at(row, p.ld_gx), k, gv[i], hv[i], rv[i], rstd, c, unused);
+    if (on && k < p.channels) backward8(p, p.gx + 2 * at(row, p.ld_gx), k, gv[i], hv[i], rv[i], rstd, mean, unused);
   }
 }
 
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_long_kernel(cons
       dot += dot8(p, k, *reinterpret_cast<const uint4*>(gy + 2 * k), *reinterpret_cast<const uint4*>(h + 2 * k));
     dot = row_sum(dot, red[flip], blockDim.x);
     flip ^= 1;
-    const float c = backward_factor(p, rstd, dot);
+    const float mean = backward_mean(p, rstd, dot);
     for (int k = t * 8; k < p.channels; k += step) {
       float4* q = reinterpret_cast<float4*>(part + k);
       float2 acc[4] = {};
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_backward_long_kernel(cons
         acc[3] = make_float2(v.z, v.w);
       }
       backward8(p, gx, k, *reinterpret_cast<const uint4*>(gy + 2 * k), *reinterpret_cast<const uint4*>(h + 2 * k),
-                gh ? *reinterpret_cast<const uint4*>(gh + 2 * k) : make_uint4(0, 0, 0, 0), rstd, c, acc);
+                gh ? *reinterpret_cast<const uint4*>(gh + 2 * k) : make_uint4(0, 0, 0, 0), rstd, mean, acc);
       q[0] = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
       q[1] = make_float4(acc[2].x, acc[2].y, acc[3].x, acc[3].y);
     }

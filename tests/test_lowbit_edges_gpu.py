@@ -52,3 +52,22 @@ def test_groups_of_zeros_among_others(g):
         assert (c[z] & 7 == 0).all()
         none = z.reshape(z.shape[0], -1, 16).all(2)
         assert none.any() and (_bytes(t).reshape(-1)[R.tile_index(*none.shape)][none] == 0x38).all()
+
+
+@pytest.mark.parametrize("rows,channels", [(6, 256), (2000, 64), (700, 6160), (3, 16400)])
+@pytest.mark.parametrize("size,grad", [(3e-20, 1.0), (1e-25, 1e-3), (1e18, 1e-6), (3e17, 1e-9)])
+def test_backward_of_tiny_and_huge_rows(rows, channels, size, grad):
+    """rstd^2 or rstd^3 would leave fp32's range here (or its normal numbers); grad_x does not.  Every product that the
+    formula names stays normal, so the errors are those of ordinary rows: half a bf16 step and, with 4 vectors of a
+    thread at most (every 1024th of a longer row), (4 + 24) 2^-24 of the magnitudes."""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    h = (torch.randn(rows, channels, generator=gen, device="cuda") * size).bfloat16()
+    gy = (torch.randn(rows, channels, generator=gen, device="cuda") * grad).bfloat16()
+    w = torch.rand(channels, generator=gen, device="cuda") + 0.5
+    rstd = torch.rsqrt(h.double().square().mean(1)).float()
+    gx, gw, mag, magw = R.norm_backward(gy, h, w, rstd, None)
+    got, gotw = sdq.rmsnorm_backward(gy, h, w, rstd)
+    assert float(gx.abs().max()) < 1e38 and got.isfinite().all()
+    # (results below 2^-126 are rounded to bf16's subnormal spacing, 2^-133)
+    assert ((got.double() - gx).abs() <= 2.0 ** -8 * gx.abs() + 28 * 2.0 ** -24 * mag + 2.0 ** -134).all()
+    assert ((gotw.double() - gw).abs() <= (-(-rows // 32) + 96) * 2.0 ** -24 * magw).all()
