@@ -219,6 +219,24 @@ __device__ __forceinline__ float4 load_shared4(uint32_t addr) {
   return v;
 }
 
+// ---- the scales per tensor ------------------------------------------------------
+
+// What the sums are multiplied by: the product of the two scales per tensor, or,
+// where that leaves fp32's normal range, first the larger and then the smaller (a
+// sum times both can be well inside: 1e-25 and 1e-18 with sums of 1e9).
+struct Alpha {
+  float pre = 1.0f, last = 1.0f;
+  __device__ __forceinline__ void set(const float* ga, const float* gb) {
+    const float a = ga ? *ga : 1.0f, b = gb ? *gb : 1.0f;
+    last = a * b;
+    if (!(fabsf(last) >= 1.17549435e-38f && fabsf(last) <= 3.40282347e38f) && a == a && b == b) {
+      pre = fmaxf(a, b);
+      last = fminf(a, b);
+    }
+  }
+  __device__ __forceinline__ float of(float sum) const { return sum * pre * last; }
+};
+
 // ---- the kernel for few rows of A -----------------------------------------------------
 //
 // Reading B bounds it, and below some 8 MB the launch and the latencies in a row
@@ -322,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     return parts + static_cast<uint32_t>(((from * kRows + row) * vecs + (vec ^ ((row >> shift) & mask))) << 4);
   };
 
+  Alpha alpha;
   if (warp == 0) {
     if (elect_one()) {
       for (int i = 0; i < steps; ++i) {
@@ -369,11 +388,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_wait(done, 0, sync.limit_ns);   // nothing of the tensor cores is in flight when the CTA frees its memory
     }
   } else {
+    alpha.set(p.ga, p.gb);   // while the sums are computed
     const bool ok = wait(sync, done, 0) && !*sync.abort;
     fence_after();
     const int quarter = warp & 3;   // the lanes a warp may read
     const int row = quarter * 32 + lane;
-    const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f);
     const int cols = static_cast<int>(min(static_cast<int64_t>(p.cols), p.rows_a - a0));
     if (ranks > 1) {
       __syncwarp();
@@ -391,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       } else if (b0 + row < p.rows_b) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (c + e < cols) mine.put(__uint_as_float(r[e]) * alpha);
+          if (c + e < cols) mine.put(alpha.of(__uint_as_float(r[e])));
       }
     }
     fence_before();
@@ -414,7 +433,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     cluster_wait();
     const int row = (warp & 3) * 32 + lane;
     if (warp >= 2 && b0 + row < p.rows_b) {
-      const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f);
       const int cols = static_cast<int>(min(static_cast<int64_t>(p.cols), p.rows_a - a0));
       const int first = rank * p.share, last = min(first + p.share, cols);
       Column out(p, a0 + first, b0 + row);
@@ -430,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float s[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (c + e < last) out.put(s[e] * alpha);
+          if (c + e < last) out.put(alpha.of(s[e]));
       }
     }
   }

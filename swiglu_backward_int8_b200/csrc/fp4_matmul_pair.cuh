@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     constexpr int kPieces = kN / 64;
     const uint32_t freed0 = at_rank(freed, 0);
     const int quarter = warp & 3, half = (warp - 2) >> 2;   // the lanes a warp may read, and which of the two it is
-    const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f);
+    Alpha alpha;
+    alpha.set(p.ga, p.gb);
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t box = ring + Z::kStages * Z::kStage + (warp - 2) * kBoxBytes;
     // The round before the first (k = -1) stores nothing: while the first tile is
@@ -333,11 +334,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           __syncwarp();
           if (lane == 0) arrive_at(freed0 + 8 * (k & 1));
         }
+        if (alpha.pre != 1.0f) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha.pre);
+        }
 #pragma unroll
         for (int h = 0; h < (kF32 ? 2 : 1); ++h) {   // an fp32 piece is two boxes
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the store before has read the box
           __syncwarp();
-          store_box<kF32>(&mo, p, box, lane, &r[32 * h], alpha, row0, col0 + piece * 64 + 32 * h);
+          store_box<kF32>(&mo, p, box, lane, &r[32 * h], alpha.last, row0, col0 + piece * 64 + 32 * h);
         }
       }
     }

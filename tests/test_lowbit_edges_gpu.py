@@ -71,3 +71,25 @@ def test_backward_of_tiny_and_huge_rows(rows, channels, size, grad):
     # (results below 2^-126 are rounded to bf16's subnormal spacing, 2^-133)
     assert ((got.double() - gx).abs() <= 2.0 ** -8 * gx.abs() + 28 * 2.0 ** -24 * mag + 2.0 ** -134).all()
     assert ((gotw.double() - gw).abs() <= (-(-rows // 32) + 96) * 2.0 ** -24 * magw).all()
+
+
+@pytest.mark.parametrize("ga,gb", [(1e-25, 1e-18), (1e-12, 1e-30), (2e-38, 0.5), (3e20, 5e19), (1e30, 1e-33), (1e-20, 0.0)])
+@pytest.mark.parametrize("m,n,k", [(20, 40, 256), (20, 40, 4096), (1700, 1600, 256)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_product_of_scales_per_tensor_past_the_range(ga, gb, m, n, k, dtype):
+    """The two scales' product leaves fp32's normal range, the output does not (or is 0).  The sums as in test_fp4_gpu;
+    two more products, 2^-24 each; half a bf16 step."""
+    gen = torch.Generator(device="cuda").manual_seed(m + k)
+    size = 1e-3 if ga > 1e15 and gb > 1e15 else 30.0
+    a, b = ((torch.randn(r, k, generator=gen, device="cuda") * size).bfloat16() for r in (m, n))
+    (a, a_s), (b, b_s) = sdq.quantize_fp4(a, "e4m3"), sdq.quantize_fp4(b, "e4m3")
+    av, bv = sdq.dequantize_fp4(a, a_s).double(), sdq.dequantize_fp4(b, b_s).double()     # (at most seven bits: exact)
+    g = [torch.tensor([v], device="cuda") for v in (ga, gb)]
+    got = sdq.matmul_fp4(a, a_s, b, b_s, a_global=g[0], b_global=g[1], out_dtype=dtype).double()
+    alpha = float(g[0].double() * g[1].double())
+    want, mag = (av @ bv.t()) * alpha, (av.abs() @ bv.abs().t()) * alpha
+    assert float(mag.max()) < 1e38
+    tol = (k / 16 + 2) * 2.0 ** -23 * mag + 2.0 ** -23 * want.abs()
+    if dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * want.abs() + 2.0 ** -134
+    assert ((got - want).abs() <= tol + 2.0 ** -149).all(), float(((got - want).abs() / tol.clamp(min=1e-300)).max())
