@@ -12,11 +12,14 @@ a shared library with a C ABI (``include/sdq.h``); the CUDA runtime is linked
 statically and the driver's tensor-map encoder is looked up at run time, so
 the library needs only the NVIDIA driver at load time.  ``csrc/marshal.cpp``, the
 short way from torch tensors to the library's entries, becomes the extension
-module ``_marshal.so`` against the installed torch.
+module ``_marshal.so`` against the installed torch, which ``_marshal.txt`` records.
+The package works without it (_extension.py): where it cannot be compiled, that is
+said and the build goes on.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import re
 import shutil
@@ -29,6 +32,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsdq.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_RECORD = os.path.join(PKG, "_marshal.txt")
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 OBJECTS = os.path.join(PKG, "_build")   # one object a source, kept for the next build
 SOURCES = [os.path.join(CSRC, f) for f in ("sdq_api.cu", "fwd_api.cu", "norm_api.cu", "fp4_api.cu")]
@@ -44,6 +48,14 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _extension():
+    """_extension.py, loaded by path: importing the package needs the library."""
+    spec = importlib.util.spec_from_file_location("sdq_extension", os.path.join(PKG, "_extension.py"))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 def _run(cmd, verbose: bool) -> None:
@@ -92,24 +104,43 @@ def _compile_marshal(verbose: bool) -> None:
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *(f"-I{i}" for i in includes), MARSHAL_SOURCE, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
           "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"], verbose)
+    if os.path.exists(MARSHAL_RECORD):   # (a new module beside an old record would not be loaded)
+        os.remove(MARSHAL_RECORD)
     os.replace(tmp, MARSHAL)
+    with open(MARSHAL_RECORD, "w") as f:
+        f.write(_extension().installed() + "\n")
+
+
+def _newer(so: str) -> bool:
+    """Whether a built file is there and newer than all sources."""
+    return os.path.exists(so) and os.path.getmtime(so) >= max(os.path.getmtime(f) for f in DEPS)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libsdq.so and _marshal.so if one is missing or older than the sources."""
-    if not force and all(os.path.exists(so) and os.path.getmtime(so) >= max(os.path.getmtime(f) for f in DEPS)
-                         for so in (LIB, MARSHAL)):
+    """Compile libsdq.so and _marshal.so, each if it is missing or older than the sources."""
+    todo = force or not _newer(LIB)
+    marshal = force or not _newer(MARSHAL) or not os.path.exists(MARSHAL_RECORD)
+    if not todo and not marshal:
         return LIB
     os.makedirs(OBJECTS, exist_ok=True)
     objects = [os.path.join(OBJECTS, os.path.basename(s) + ".o") for s in SOURCES]
     with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as pool:
-        marshal = pool.submit(_compile_marshal, verbose)
-        for _ in pool.map(lambda so: _compile(*so, force, verbose), zip(SOURCES, objects)):
-            pass
-        marshal.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    _run([nvcc(), *ARCH, "-shared", *objects, "-o", tmp], verbose)
-    os.replace(tmp, LIB)
+        short = pool.submit(_compile_marshal, verbose) if marshal else None
+        if todo:
+            for _ in pool.map(lambda so: _compile(*so, force, verbose), zip(SOURCES, objects)):
+                pass
+        try:
+            if short:
+                short.result()
+        except Exception as e:   # no torch headers, no host compiler, ...
+            for f in (MARSHAL, MARSHAL_RECORD):
+                if os.path.exists(f):
+                    os.remove(f)
+            sys.stderr.write(f"{MARSHAL} was not built, the package goes without it:\n{e}\n")
+    if todo:
+        tmp = LIB + f".tmp{os.getpid()}"
+        _run([nvcc(), *ARCH, "-shared", *objects, "-o", tmp], verbose)
+        os.replace(tmp, LIB)
     return LIB
 
 

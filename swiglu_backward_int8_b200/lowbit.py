@@ -19,7 +19,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _marshal
+from . import _extension
 from ._check import _rows
 from ._lib import (FMT_E2M1, FMT_E4M3, FMT_E8M0, FMT_OUT_F32, FMT_SCALE_E4M3, FMT_WEIGHT_F32,
                    SdqError, entry_addresses, sdq_dequantize_fp4, sdq_matmul_fp4, sdq_quantize_fp4, sdq_rmsnorm_backward,
@@ -28,7 +28,7 @@ from ._lib import (FMT_E2M1, FMT_E4M3, FMT_E8M0, FMT_OUT_F32, FMT_SCALE_E4M3, FM
 # Each function below first offers its arguments to its namesake in csrc/marshal.cpp,
 # which makes the ordinary call (every output given, on the current device) and
 # answers with its status, or with -1: then the checks and allocations here run.
-_marshal.bind(*entry_addresses())
+_marshal = _extension.load(entry_addresses())
 
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
