@@ -36,7 +36,7 @@ MARSHAL_RECORD = os.path.join(PKG, "_marshal.txt")
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 OBJECTS = os.path.join(PKG, "_build")   # one object a source, kept for the next build
 SOURCES = [os.path.join(CSRC, f) for f in ("sdq_api.cu", "fwd_api.cu", "norm_api.cu", "fp4_api.cu")]
-DEPS = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)) + [os.path.join(INCLUDE, "sdq.h")]
+DEPS = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)) + [os.path.join(INCLUDE, "sdq.h"), os.path.abspath(__file__)]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -116,10 +116,19 @@ def _newer(so: str) -> bool:
     return os.path.exists(so) and os.path.getmtime(so) >= max(os.path.getmtime(f) for f in DEPS)
 
 
+def _marshal_fits() -> bool:
+    """Whether _marshal.so is newer than the sources and was built for this torch."""
+    if not _newer(MARSHAL):
+        return False
+    e = _extension()
+    return e.built_for(MARSHAL, MARSHAL_RECORD) == e.installed()
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libsdq.so and _marshal.so, each if it is missing or older than the sources."""
+    """Compile libsdq.so if it is missing or older than the sources, and
+    _marshal.so likewise, or if it was built for another torch."""
     todo = force or not _newer(LIB)
-    marshal = force or not _newer(MARSHAL) or not os.path.exists(MARSHAL_RECORD)
+    marshal = force or not _marshal_fits()
     if not todo and not marshal:
         return LIB
     os.makedirs(OBJECTS, exist_ok=True)

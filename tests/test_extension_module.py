@@ -119,3 +119,18 @@ def test_build_goes_on_without_the_module(tree, capfd):
     assert "_marshal.so was not built" in capfd.readouterr().err
     assert tree() == ["_marshal.so"]                     # tried again, alone
     assert tree() == []
+
+
+def test_build_makes_the_module_anew_for_another_torch(tree):
+    assert tree() == ALL and tree() == []
+    (tree.pkg / "_marshal.txt").write_text("torch 2.10.0, C++ ABI 1, Python cpython-312\n")
+    assert tree() == ["_marshal.so"] and tree() == []
+    (tree.pkg / "_marshal.txt").unlink()
+    assert tree() == ["_marshal.so"] and tree() == []
+
+
+def test_build_makes_all_anew_after_a_change_of_its_flags(tree):
+    assert tree() == ALL
+    later = os.path.getmtime(tree.pkg / "libsdq.so") + 10
+    os.utime(tree.pkg / "build.py", (later, later))
+    assert tree() == ALL
