@@ -7,6 +7,10 @@
 // the Python code then handles or refuses with its reason.  The same checks in
 // Python cost 5 us a call, twice what such a call's kernel takes.
 //
+// The interpreter's lock is given back around the C entry: a launch waits while
+// the stream's queue is full, and what the queue waits for may need the lock (a
+// host function, another thread's launch).
+//
 // The C entries' addresses come from the loaded library (bind).
 #include <Python.h>
 
@@ -29,6 +33,18 @@ decltype(&sdq_rmsnorm_backward_workspace_bytes) g_workspace_bytes;
 decltype(&sdq_quantize_fp4) g_quantize;
 decltype(&sdq_dequantize_fp4) g_dequantize;
 decltype(&sdq_matmul_fp4) g_matmul;
+
+// f(args...) without the interpreter's lock; the arguments are made before it is
+// given back.  (The caller's references keep the tensors alive.)
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <class F, class... A>
+int unlocked(F f, A... args) {
+  const Unlocked u;
+  return f(args...);
+}
 
 struct Unusual {};   // thrown inside a function here, answered with -1 by its caller
 
@@ -151,10 +167,10 @@ int norm(PyObject* const* a) {
     if (t.scalar_type() != at::kFloat) throw Unusual();
     rstd = static_cast<const float*>(vector_of(t, rows, dev));
   }
-  return g_norm(ox.p, ox.ld, residual.p, residual.ld, wp, const_cast<void*>(h.p), h.ld, const_cast<void*>(oq.p), oq.ld,
-                const_cast<void*>(os.p), os.ld, const_cast<void*>(y.p), y.ld, const_cast<float*>(rstd),
-                global_of(a[12], s4, dev), rows, channels, static_cast<int32_t>(given), fmt, static_cast<float>(eps),
-                stream(dev));
+  return unlocked(g_norm, ox.p, ox.ld, residual.p, residual.ld, wp, const_cast<void*>(h.p), h.ld, const_cast<void*>(oq.p),
+                  oq.ld, const_cast<void*>(os.p), os.ld, const_cast<void*>(y.p), y.ld, const_cast<float*>(rstd),
+                  global_of(a[12], s4, dev), rows, channels, static_cast<int32_t>(given), fmt, static_cast<float>(eps),
+                  stream(dev));
 }
 
 // grad_y, h, weight, rstd, grad_h, grad_x, grad_weight, workspace
@@ -184,9 +200,9 @@ int norm_backward(PyObject* const* a) {
     on(ws, dev);
     if (!ws.is_contiguous()) throw Unusual();
   }
-  return g_norm_backward(ogy.p, ogy.ld, oh.p, oh.ld, wp, rp, ogh.p, ogh.ld, const_cast<void*>(ogx.p), ogx.ld, gp, rows,
-                         channels, f32 ? SDQ_FMT_WEIGHT_F32 : 0, ws.data_ptr(),
-                         static_cast<size_t>(ws.numel() * ws.element_size()), stream(dev));
+  return unlocked(g_norm_backward, ogy.p, ogy.ld, oh.p, oh.ld, wp, rp, ogh.p, ogh.ld, const_cast<void*>(ogx.p), ogx.ld, gp,
+                  rows, channels, f32 ? SDQ_FMT_WEIGHT_F32 : 0, ws.data_ptr(),
+                  static_cast<size_t>(ws.numel() * ws.element_size()), stream(dev));
 }
 
 void fp4_length(int64_t k) {
@@ -220,9 +236,9 @@ int quantize(PyObject* const* a) {
     qt = rows_of(tensor(a[5]), channels, padded / 2, at::kByte, dev);
     st = tiles_of(tensor(a[6]), channels, padded, e4m3, dev);
   }
-  return g_quantize(ox.p, ox.ld, const_cast<void*>(q.p), q.ld, const_cast<void*>(s), const_cast<void*>(qt.p), qt.ld,
-                    const_cast<void*>(st), global_of(a[7], e4m3, dev), rows, channels,
-                    e4m3 ? SDQ_FMT_SCALE_E4M3 : SDQ_FMT_E8M0, stream(dev));
+  return unlocked(g_quantize, ox.p, ox.ld, const_cast<void*>(q.p), q.ld, const_cast<void*>(s), const_cast<void*>(qt.p),
+                  qt.ld, const_cast<void*>(st), global_of(a[7], e4m3, dev), rows, channels,
+                  e4m3 ? SDQ_FMT_SCALE_E4M3 : SDQ_FMT_E8M0, stream(dev));
 }
 
 // q, s, global_scale, out
@@ -236,8 +252,8 @@ int dequantize(PyObject* const* a) {
   const Operand oq = rows_of(q, rows, k / 2, at::kByte, dev);
   const void* sp = tiles_of(s, rows, k, e4m3, dev);
   const Operand out = rows_of(tensor(a[3]), rows, k, at::kBFloat16, dev);
-  return g_dequantize(oq.p, oq.ld, sp, global_of(a[2], e4m3, dev), const_cast<void*>(out.p), out.ld, rows, k,
-                      e4m3 ? SDQ_FMT_SCALE_E4M3 : SDQ_FMT_E8M0, stream(dev));
+  return unlocked(g_dequantize, oq.p, oq.ld, sp, global_of(a[2], e4m3, dev), const_cast<void*>(out.p), out.ld, rows, k,
+                  e4m3 ? SDQ_FMT_SCALE_E4M3 : SDQ_FMT_E8M0, stream(dev));
 }
 
 // a, a_s, b, b_s, a_global, b_global, out, out_dtype
@@ -253,7 +269,7 @@ int matmul(PyObject* const* a) {
   const Operand oa = rows_of(qa, m, k / 2, at::kByte, dev), ob = rows_of(qb, n, k / 2, at::kByte, dev);
   const void *ap = tiles_of(sa, m, k, e4m3, dev), *bp = tiles_of(sb, n, k, e4m3, dev);
   const Operand oo = rows_of(out, m, n, f32 ? at::kFloat : at::kBFloat16, dev);
-  return g_matmul(oa.p, oa.ld, ap, global_of(a[4], e4m3, dev), ob.p, ob.ld, bp, global_of(a[5], e4m3, dev),
+  return unlocked(g_matmul, oa.p, oa.ld, ap, global_of(a[4], e4m3, dev), ob.p, ob.ld, bp, global_of(a[5], e4m3, dev),
                   const_cast<void*>(oo.p), oo.ld, m, n, k,
                   (e4m3 ? SDQ_FMT_SCALE_E4M3 : SDQ_FMT_E8M0) | (f32 ? SDQ_FMT_OUT_F32 : 0u), stream(dev));
 }
