@@ -120,13 +120,13 @@ __device__ __forceinline__ void load_weight(const uint8_t* weight, int f32, int3
     const float4* q = reinterpret_cast<const float4*>(weight + 4 * k);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldg(q + i);
+      const float4 v = q[i];
       w[2 * i] = make_float2(v.x, v.y);
       w[2 * i + 1] = make_float2(v.z, v.w);
     }
   } else {
     const uint4* q = reinterpret_cast<const uint4*>(weight + 2 * k);
-    unpack({__ldg(q), __ldg(q + 1)}, w);
+    unpack({q[0], q[1]}, w);
   }
 }
 
@@ -369,14 +369,14 @@ struct BwdParams {
 
 __device__ __forceinline__ void load_weight8(const uint8_t* weight, int f32, int32_t k, float2 (&w)[4]) {
   if (f32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(weight + 4 * k));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(weight + 4 * k) + 1);
+    const float4 a = *reinterpret_cast<const float4*>(weight + 4 * k);
+    const float4 b = *(reinterpret_cast<const float4*>(weight + 4 * k) + 1);
     w[0] = make_float2(a.x, a.y);
     w[1] = make_float2(a.z, a.w);
     w[2] = make_float2(b.x, b.y);
     w[3] = make_float2(b.z, b.w);
   } else {
-    quant::unpack8(__ldg(reinterpret_cast<const uint4*>(weight + 2 * k)), w);
+    quant::unpack8(*reinterpret_cast<const uint4*>(weight + 2 * k), w);
   }
 }
 

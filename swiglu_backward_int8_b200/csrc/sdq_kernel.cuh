@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t slot = n % STAGES;
     float dsc = 0.0f;   // INT8 grad_y: the scale of this lane's row in tile column j
     if constexpr (kQdy) {
-      if (r < valid) dsc = __ldg(p.gys + (row0 + r) * p.ld_gys + j);
+      if (r < valid) dsc = p.gys[(row0 + r) * p.ld_gys + j];
     }
     ok = __all_sync(kFull, wait_or_abort(smem_u32(&s.full[0][0] + ring_bar_index(n, STAGES)),
                                          ring_parity(n, STAGES), lim, abort_flag));

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = sub * kStageRows2 + srow;   // this lane's row within the unit
       float dsc = 0.0f;
       if constexpr (kQdy) {   // INT8 grad_y: its scale per token and 128 channels
-        if (r < valid && j * kG2 + 16 * cq < K) dsc = __ldg(p.gys + (row0 + r) * p.ld_gys + 2 * j + (cq >> 3));
+        if (r < valid && j * kG2 + 16 * cq < K) dsc = p.gys[(row0 + r) * p.ld_gys + 2 * j + (cq >> 3)];
       }
       ok = __all_sync(kFull, wait_or_abort(smem_u32(&s.full[0][0] + ring_bar_index(n, STAGES)),
                                            ring_parity(n, STAGES), lim, abort_flag));

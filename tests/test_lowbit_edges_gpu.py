@@ -93,3 +93,26 @@ def test_product_of_scales_per_tensor_past_the_range(ga, gb, m, n, k, dtype):
     if dtype == torch.bfloat16:
         tol = tol + 2.0 ** -8 * want.abs() + 2.0 ** -134
     assert ((got - want).abs() <= tol + 2.0 ** -149).all(), float(((got - want).abs() / tol.clamp(min=1e-300)).max())
+
+
+def test_norm_of_a_weight_that_the_kernel_before_writes():
+    """The weight's memory changes in each call before the norm; both kernels may overlap up to the norm's wait."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x, gy = (torch.randn(900, 4096, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    base = torch.randn(1, 4096, generator=gen, device="cuda")
+    codes = [sdq.quantize_fp4((base * f).bfloat16()) for f in (1, -2)]
+    weights = [sdq.dequantize_fp4(*c) for c in codes]
+    rstd = torch.empty(900, device="cuda")
+    want = [(sdq.rmsnorm_quant(x, w[0], rstd=rstd)[0], *sdq.rmsnorm_backward(gy, x, w[0], rstd)) for w in weights]
+    w = torch.empty_like(weights[0])
+    for _ in range(10):
+        got = []
+        for i in range(20):
+            sdq.dequantize_fp4(*codes[i & 1], out=w)
+            q = sdq.rmsnorm_quant(x, w[0])[0]
+            sdq.dequantize_fp4(*codes[1 - (i & 1)], out=w)
+            sdq.dequantize_fp4(*codes[i & 1], out=w)
+            got.append((q, *sdq.rmsnorm_backward(gy, x, w[0], rstd)))
+        torch.cuda.synchronize()
+        for i, outs in enumerate(got):
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i & 1])), i
