@@ -186,6 +186,10 @@ __device__ __forceinline__ bool wait(const Sync& y, uint32_t bar, uint32_t parit
   return true;
 }
 
+// Whether all lanes say so: each decides by itself whether its wait has run out, and
+// what follows takes the warp together (tcgen05.ld, a barrier of the cluster).
+__device__ __forceinline__ bool all_lanes(bool v) { return __all_sync(0xffffffffu, v); }
+
 // ---- clusters -----------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else {
     alpha.set(p.ga, p.gb);   // while the sums are computed
-    const bool ok = wait(sync, done, 0) && !*sync.abort;
+    const bool ok = all_lanes(wait(sync, done, 0) && !*sync.abort);
     fence_after();
     const int quarter = warp & 3;   // the lanes a warp may read
     const int row = quarter * 32 + lane;

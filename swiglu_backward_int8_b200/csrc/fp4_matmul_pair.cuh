@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     // finds cold (1100 cycles at the end of a call that has one tile).
     for (int k = -1;; ++k) {
       const int t = first + k * stride;
-      if (k >= 0 && (t >= tiles || !wait(sync, sums + 8 * (k & 1), (k >> 1) & 1))) break;
+      if (k >= 0 && (t >= tiles || !all_lanes(wait(sync, sums + 8 * (k & 1), (k >> 1) & 1)))) break;
       fence_after();
       const int tb = t / p.tiles_a, ta = t - tb * p.tiles_a;
       const int64_t row0 = k < 0 ? p.rows_a : static_cast<int64_t>(ta) * 256 + rank * 128 + quarter * 32;
