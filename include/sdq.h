@@ -556,6 +556,20 @@ int sdq_fuse_test_stall(const void* x, const void* grad_y, int8_t* grad_input_q,
                         int64_t K, int32_t group_size, int64_t wait_limit_ns, void* stream);
 
 /*
+ * sdq_matmul_fp4_test_stall -- test hook for the failure path of
+ * sdq_matmul_fp4 (without scales per tensor): in every cluster of the kernel's
+ * CTAs, CTA `rank` withholds its loads from number `step` on (0: all; CTAs of
+ * fewer loads are not held up), so that waits run out after `wait_limit_ns` (1 us
+ * .. 1 s; outside that, or with a negative rank or step, SDQ_ERR_SHAPE).  The
+ * kernel waits for what it has in flight and stops early; the rest as
+ * sdq_fuse_test_stall.
+ */
+int sdq_matmul_fp4_test_stall(const void* a, int64_t ld_a, const void* a_s, const void* b, int64_t ld_b,
+                              const void* b_s, void* out, int64_t ld_out, int64_t m, int64_t n,
+                              int64_t k, uint32_t format, int32_t rank, int32_t step,
+                              int64_t wait_limit_ns, void* stream);
+
+/*
  * sdq_device_status -- synchronizes `stream`, then reads and clears the
  * device-side status word of the current device: SDQ_OK, or
  * SDQ_ERR_TIMEOUT if a kernel's wait on its shared-memory pipeline ran past

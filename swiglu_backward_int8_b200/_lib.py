@@ -60,6 +60,8 @@ for _name, _args, _more in (("rmsnorm_quant", _NORM, [_F32, _P]), ("rmsnorm_back
     getattr(_lib, f"sdq_{_name}").restype = ctypes.c_int
     getattr(_lib, f"sdq_validate_{_name}").argtypes = _args
     getattr(_lib, f"sdq_validate_{_name}").restype = ctypes.c_int
+_lib.sdq_matmul_fp4_test_stall.argtypes = [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _U32, _I32, _I32, _I64, _P]
+_lib.sdq_matmul_fp4_test_stall.restype = ctypes.c_int
 _lib.sdq_rmsnorm_backward_workspace_bytes.argtypes = [_I64, _I64]
 _lib.sdq_rmsnorm_backward_workspace_bytes.restype = ctypes.c_size_t
 _lib.sdq_fp4_scale_bytes.argtypes = [_I64, _I64, _U32]
@@ -304,6 +306,11 @@ def sdq_rmsnorm_backward_workspace_bytes(rows: int, channels: int) -> int:
 
 def sdq_fp4_scale_bytes(rows: int, k: int, format: int) -> int:
     return int(_lib.sdq_fp4_scale_bytes(rows, k, format))
+
+
+def sdq_matmul_fp4_test_stall(*args) -> None:
+    """Test hook (include/sdq.h): the product with one CTA's loads withheld."""
+    _check(_lib.sdq_matmul_fp4_test_stall(*args), "sdq_matmul_fp4_test_stall")
 
 
 def entry_addresses() -> tuple:

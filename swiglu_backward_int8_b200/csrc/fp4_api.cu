@@ -80,6 +80,8 @@ struct Product {
   int64_t m, n, k;
   uint32_t format;
   cudaStream_t stream;
+  int32_t stall_step = -1, stall_rank = -1;   // a test's: sdq_matmul_fp4_test_stall
+  uint64_t wait_limit = sdq_internal::wait_limit();
 };
 
 // Many tiles: pairs of multiprocessors.
@@ -99,7 +101,9 @@ int launch_pair(const Product& c, int sms) {
   p.tiles_b = static_cast<int32_t>((c.n + sdq::mm4::kN - 1) / sdq::mm4::kN);
   const uintptr_t at = reinterpret_cast<uintptr_t>(c.out) | static_cast<uintptr_t>(c.ld_out * (kF32 ? 4 : 2));
   p.vec = at & 15 ? 0 : 1;
-  p.wait_limit_ns = sdq_internal::wait_limit();
+  p.stall_step = c.stall_step;
+  p.stall_rank = c.stall_rank;
+  p.wait_limit_ns = c.wait_limit;
   if (const int e = sdq_internal::device_status_word(&p.status)) return e;
   CUtensorMap ma, mb, msa, msb, mo = {};
   if (const int e = sdq_internal::make_code_map(&ma, c.a, c.k / 2, c.m, c.ld_a, 128)) return e;
@@ -135,7 +139,9 @@ int launch_strip(const Product& c, int sms) {
   p.tiles_b = static_cast<int32_t>((c.n + 127) / 128);
   p.stage = Z::stage(p.cols);
   p.out_f32 = c.format & SDQ_FMT_OUT_F32 ? 1 : 0;
-  p.wait_limit_ns = sdq_internal::wait_limit();
+  p.stall_step = c.stall_step;
+  p.stall_rank = c.stall_rank;
+  p.wait_limit_ns = c.wait_limit;
   if (const int e = sdq_internal::device_status_word(&p.status)) return e;
   CUtensorMap ma, mb;
   if (const int e = sdq_internal::make_code_map(&mb, c.b, c.k / 2, c.n, c.ld_b, 128)) return e;
@@ -159,6 +165,19 @@ int launch_strip(const Product& c, int sms) {
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage + Z::sums(p.cols, split);
   void* args[] = {&mb, &ma, &p};
   return launch(fn, static_cast<unsigned>(tiles * split), sdq::mm4::kThreads, smem, c.stream, args, split);
+}
+
+int launch_product(const Product& c) {
+  int sms = 0;
+  if (const int e = sdq_internal::sm_count(&sms)) return e;
+  const bool e8m0 = c.format & SDQ_FMT_E8M0, f32 = c.format & SDQ_FMT_OUT_F32;
+  // Tiles of 128 x 128 that the device takes at once: 128 columns a CTA keep more
+  // multiprocessors busy than 256 x 256 outputs a pair (256 x 1024 x 1024: 5.1 us
+  // instead of 5.7; 1024 x 1024 x 4096: 9.4 instead of 9.8).
+  if (c.m <= 128 || (c.m + 127) / 128 * ((c.n + 127) / 128) <= sms)
+    return e8m0 ? launch_strip<Scales::kE8M0>(c, sms) : launch_strip<Scales::kE4M3>(c, sms);
+  if (f32) return e8m0 ? launch_pair<Scales::kE8M0, true>(c, sms) : launch_pair<Scales::kE4M3, true>(c, sms);
+  return e8m0 ? launch_pair<Scales::kE8M0, false>(c, sms) : launch_pair<Scales::kE4M3, false>(c, sms);
 }
 
 }  // namespace
@@ -272,16 +291,18 @@ int sdq_matmul_fp4(const void* a, int64_t ld_a, const void* a_s, const float* a_
                    uint32_t format, void* stream) {
   const int st = sdq_validate_matmul_fp4(a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format);
   if (st != SDQ_OK || m == 0 || n == 0) return st;
-  int sms = 0;
-  if (const int e = sdq_internal::sm_count(&sms)) return e;
-  const Product c = {a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format, static_cast<cudaStream_t>(stream)};
-  const bool e8m0 = format & SDQ_FMT_E8M0, f32 = format & SDQ_FMT_OUT_F32;
-  // Tiles of 128 x 128 that the device takes at once: 128 columns a CTA keep more
-  // multiprocessors busy than 256 x 256 outputs a pair (256 x 1024 x 1024: 5.1 us
-  // instead of 5.7; 1024 x 1024 x 4096: 9.4 instead of 9.8).
-  if (m <= 128 || (m + 127) / 128 * ((n + 127) / 128) <= sms) return e8m0 ? launch_strip<Scales::kE8M0>(c, sms) : launch_strip<Scales::kE4M3>(c, sms);
-  if (f32) return e8m0 ? launch_pair<Scales::kE8M0, true>(c, sms) : launch_pair<Scales::kE4M3, true>(c, sms);
-  return e8m0 ? launch_pair<Scales::kE8M0, false>(c, sms) : launch_pair<Scales::kE4M3, false>(c, sms);
+  return launch_product({a, ld_a, a_s, a_global, b, ld_b, b_s, b_global, out, ld_out, m, n, k, format,
+                         static_cast<cudaStream_t>(stream)});
+}
+
+int sdq_matmul_fp4_test_stall(const void* a, int64_t ld_a, const void* a_s, const void* b, int64_t ld_b, const void* b_s,
+                              void* out, int64_t ld_out, int64_t m, int64_t n, int64_t k, uint32_t format, int32_t rank,
+                              int32_t step, int64_t wait_limit_ns, void* stream) {
+  const int st = sdq_validate_matmul_fp4(a, ld_a, a_s, nullptr, b, ld_b, b_s, nullptr, out, ld_out, m, n, k, format);
+  if (st != SDQ_OK || m == 0 || n == 0) return st;
+  if (rank < 0 || step < 0 || wait_limit_ns < 1000 || wait_limit_ns > 1000000000) return SDQ_ERR_SHAPE;
+  return launch_product({a, ld_a, a_s, nullptr, b, ld_b, b_s, nullptr, out, ld_out, m, n, k, format,
+                         static_cast<cudaStream_t>(stream), step, rank, static_cast<uint64_t>(wait_limit_ns)});
 }
 
 }  // extern "C"

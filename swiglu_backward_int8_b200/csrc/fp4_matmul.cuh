@@ -45,6 +45,7 @@ struct Params {
   int32_t stages, stage;   // the shared-memory ring
   int32_t share, share_log;   // columns that belong to a CTA of a cluster: a power of two
   int32_t out_f32;         // fp32 elements instead of bf16
+  int32_t stall_step, stall_rank;   // the first load that this CTA of a cluster withholds (a test's; else -1)
   int* status;
   uint64_t wait_limit_ns;
 };
@@ -159,37 +160,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// ---- waits ----------------------------------------------------------------------
-
-struct Sync {
-  int* status;         // the device status word
-  volatile int* abort; // shared: set by the first wait that runs out
-  uint64_t limit_ns;
-};
-
-// Waits for the barrier's phase, no longer than the limit; false once any
-// wait of the CTA has run out.
-__device__ __forceinline__ bool wait(const Sync& y, uint32_t bar, uint32_t parity) {
-  // (a try_wait suspends the thread for a while by itself; the timer, slow to
-  // read, comes in only once several have run out)
-  for (int i = 0; i < 32; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*y.abort) return false;
-    if (globaltimer_ns() - t0 > y.limit_ns) {
-      *y.abort = 1;
-      atomicOr(y.status, 1);
-      return false;
-    }
-  }
-  return true;
-}
-
-// Whether all lanes say so: each decides by itself whether its wait has run out, and
-// what follows takes the warp together (tcgen05.ld, a barrier of the cluster).
-__device__ __forceinline__ bool all_lanes(bool v) { return __all_sync(0xffffffffu, v); }
-
 // ---- clusters -----------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -217,11 +187,57 @@ __device__ __forceinline__ void store_cluster4(uint32_t addr, const uint32_t* v)
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                : "memory");
 }
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ float4 load_shared4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
+
+// ---- waits ----------------------------------------------------------------------
+
+struct Sync {
+  int* status;         // the device status word
+  volatile int* abort; // shared: set by the first wait that runs out
+  uint64_t limit_ns;
+};
+
+// Waits for the barrier's phase, no longer than the limit; false once any
+// wait of the CTA has run out.
+__device__ __forceinline__ bool wait(const Sync& y, uint32_t bar, uint32_t parity) {
+  // (a try_wait suspends the thread for a while by itself; the timer, slow to
+  // read, comes in only once several have run out)
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*y.abort) return false;
+    if (globaltimer_ns() - t0 > y.limit_ns) {
+      *y.abort = 1;
+      atomicOr(y.status, 1);
+      return false;
+    }
+  }
+  return true;
+}
+
+// What a CTA has in flight when a wait has run out (copies into its shared memory,
+// signals to its barriers) lands before it leaves: waited for, in all no longer
+// than a second, however short the waits' own limit.
+struct Drain {
+  static constexpr uint64_t kLimitNs = 1000000000;
+  const uint64_t t0 = globaltimer_ns();
+  __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) const {
+    const uint64_t used = globaltimer_ns() - t0;
+    mbar_wait(bar, parity, used < kLimitNs ? kLimitNs - used : 0);
+  }
+};
+
+// Whether all lanes say so: each decides by itself whether its wait has run out, and
+// what follows takes the warp together (tcgen05.ld, a barrier of the cluster).
+__device__ __forceinline__ bool all_lanes(bool v) { return __all_sync(0xffffffffu, v); }
 
 // ---- the scales per tensor ------------------------------------------------------
 
@@ -349,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (elect_one()) {
       for (int i = 0; i < steps; ++i) {
         const int st = i % p.stages, step = rank + i * ranks;
+        if (i == p.stall_step && rank == p.stall_rank) break;
         if (i >= p.stages && !wait(sync, empty + 8 * st, ((i / p.stages) - 1) & 1)) break;
         const uint32_t buf = ring + st * p.stage, bar = full + 8 * st;
         const int k_tile = step * Z::kScaleTiles;
@@ -389,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         commit(empty + 8 * st);
       }
       commit(done);
-      mbar_wait(done, 0, sync.limit_ns);   // nothing of the tensor cores is in flight when the CTA frees its memory
+      Drain().wait(done, 0);   // nothing of the tensor cores is in flight when the CTA frees its memory
     }
   } else {
     alpha.set(p.ga, p.gb);   // while the sums are computed
@@ -457,8 +474,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   if (threadIdx.x == 0 && abort_flag) {   // copies still in flight write this CTA's shared memory
+    const Drain drain;
     for (int i = max(0, issued_flag - p.stages); i < issued_flag; ++i)
-      mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1, sync.limit_ns);
+      drain.wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
   }
 }
 

@@ -61,6 +61,7 @@ struct PairParams {
   int32_t codes;
   int32_t tiles_a, tiles_b;
   int32_t vec;             // the output's rows start on 16 bytes: bulk stores
+  int32_t stall_step, stall_rank;   // the first load that this CTA of a pair withholds (a test's; else -1)
   int* status;
   uint64_t wait_limit_ns;
 };
@@ -78,6 +79,10 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "[%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(cluster_bar)
       : "memory");
+}
+// Counts bytes on a barrier of this CTA as landed that will not come.
+__device__ __forceinline__ void complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void commit_pair(uint32_t cluster_bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(cluster_bar) : "memory");
@@ -188,6 +193,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   __shared__ alignas(8) uint64_t bars[2 * Z::kStages + 4];
   __shared__ uint32_t tmem_addr;
   __shared__ int abort_flag;
+  // for the end after a wait that ran out: loads that either CTA has issued (in the
+  // first CTA), steps and tiles that the tensor cores have been given (in both)
+  __shared__ int issued[2], stepped, tiled;
   // the ring starts at the same offset in both CTAs: descriptors hold for the pair
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t full = smem_u32(bars), empty = full + 8 * Z::kStages, sums = empty + 8 * Z::kStages, freed = sums + 16;
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_init(freed, 2 * kEpilogueWarps);
     mbar_init(freed + 8, 2 * kEpilogueWarps);
     fence_mbar_init();
-    abort_flag = 0;
+    abort_flag = issued[0] = issued[1] = stepped = tiled = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_addr)), "r"(512u)
@@ -226,11 +234,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   if (warp == 0) {
     if (elect_one()) {
       const uint32_t full0 = at_rank(full, 0);
+      const int most = static_cast<int>(rank) == p.stall_rank ? p.stall_step : INT32_MAX;
       int n = 0;   // loads so far
       bool ok = true;
       for (int t = first; t < tiles && ok; t += stride) {
         const int tb = t / p.tiles_a, ta = t - tb * p.tiles_a;
-        for (int i = 0; i < steps; ++i, ++n) {
+        const int here = min(steps, most - n);   // (in the loop: 8192 x 14336 x 4096 176.5 us, so 174.2)
+        for (int i = 0; i < here; ++i, ++n) {
           const int st = n % Z::kStages;
           if (n >= Z::kStages) ok = wait(sync, empty + 8 * st, ((n / Z::kStages) - 1) & 1);
           if (!ok) break;
@@ -244,8 +254,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           for (int b = 0; b < Z::kBlocksB; ++b)
             tma_load_pair(sc + Z::kScaleA + b * Z::kScaleA, &msb, bar, i * (Z::kScaleA / 8), tb * Z::kBlocksB + b);
         }
+        ok = ok && here == steps;
       }
-      // every load this thread has issued has landed, or its wait has run out
+      store_cluster(at_rank(smem_u32(&issued[rank]), 0), static_cast<uint32_t>(n));
+      // every load this thread has issued has landed, or a wait has run out
       if (ok)
         for (int i = n > Z::kStages ? n - Z::kStages : 0; i < n && ok; ++i)
           ok = wait(sync, empty + 8 * (i % Z::kStages), (i / Z::kStages) & 1);
@@ -287,10 +299,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           commit_pair(empty + 8 * st);
           commit_pair(empty1 + 8 * st);
         }
-        if (ok) {
-          commit_pair(sums + 8 * (k & 1));
-          commit_pair(sums1 + 8 * (k & 1));
-        }
+        if (!ok) break;
+        commit_pair(sums + 8 * (k & 1));
+        commit_pair(sums1 + 8 * (k & 1));
+      }
+      for (uint32_t r = 0; r < 2; ++r) {   // (read after a barrier of the cluster, if at all)
+        store_cluster(at_rank(smem_u32(&stepped), r), static_cast<uint32_t>(n));
+        store_cluster(at_rank(smem_u32(&tiled), r), static_cast<uint32_t>(k));
       }
     }
   } else {
@@ -350,12 +365,31 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   }
   // neither CTA leaves while the other may still signal its barriers or use its memory
   __syncthreads();
-  if (abort_flag && threadIdx.x == 0) {   // a wait ran out: give what is in flight the same time to land
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < p.wait_limit_ns) __nanosleep(1000);
-  }
-  __syncthreads();
+  if (threadIdx.x == 0 && *sync.abort) store_cluster(at_rank(smem_u32(&abort_flag), rank ^ 1), 1u);
+  __syncwarp();
   cluster_sync();
+  // A wait ran out, and both CTAs know: what is in flight lands before either goes on.
+  // (A phase waited for here is its barrier's present one or the last: step i was
+  // given to the tensor cores, and load i issued, after step i - stages was done.)
+  if (*sync.abort) {
+    if (threadIdx.x == 0) {
+      const Drain drain;
+      for (int i = max(0, stepped - Z::kStages); i < stepped; ++i)   // products, and their signals to this CTA
+        drain.wait(empty + 8 * (i % Z::kStages), (i / Z::kStages) & 1);
+      for (int k = max(0, tiled - 2); k < tiled; ++k) drain.wait(sums + 8 * (k & 1), (k >> 1) & 1);
+      if (rank == 0) {   // loads of both CTAs; where one has not issued its half, only the other's bytes come
+        const int loads = max(issued[0], issued[1]);
+        for (int i = max(0, loads - Z::kStages); i < loads; ++i) {
+          const uint32_t bar = full + 8 * (i % Z::kStages);
+          if (i >= issued[0]) mbar_arrive_expect_tx(bar, Z::kStage);
+          if (i >= issued[1]) complete_tx(bar, Z::kStage);
+          drain.wait(bar, (i / Z::kStages) & 1);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   __syncwarp();
   if (warp == 1) {
     fence_after();
