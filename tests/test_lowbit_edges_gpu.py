@@ -116,3 +116,46 @@ def test_norm_of_a_weight_that_the_kernel_before_writes():
         torch.cuda.synchronize()
         for i, outs in enumerate(got):
             assert all(torch.equal(a, b) for a, b in zip(outs, want[i & 1])), i
+
+
+def test_residual_sum_of_any_bits():
+    """h = bf16(x + residual) for every kind of number: subnormals, both zeros, infinities, sums that overflow, ties."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    rows, channels = 300, 1024
+    x, r = (torch.randint(-32768, 32768, (rows, channels), generator=gen, device="cuda", dtype=torch.int16).view(torch.bfloat16)
+            for _ in range(2))
+    r[:100] = (x[:100].float() * (torch.randint(-4, 5, (100, channels), generator=gen, device="cuda") * 0.00390625)).bfloat16()
+    r[100:150] = -x[100:150]
+    small = torch.randint(0, 512, (2, 50, channels), generator=gen, device="cuda", dtype=torch.int16)     # below 2^-124
+    x[150:200], r[150:200] = small[0].view(torch.bfloat16), -small[1].view(torch.bfloat16)
+    for n in (rows, 3):
+        _, _, h = sdq.rmsnorm_quant(x[-n:], torch.ones(channels, device="cuda"), r[-n:])
+        want = (x[-n:].float() + r[-n:].float()).bfloat16()
+        assert torch.equal(h.isnan(), want.isnan())
+        assert torch.equal(h[~want.isnan()].view(torch.int16), want[~want.isnan()].view(torch.int16))
+
+
+def _sums(m, n, k, scales, bytes_a, bytes_b, seed):
+    """The product of random codes with scale bytes of two ranges, and its 64-bit form."""
+    rng = np.random.default_rng(seed)
+    out = []
+    for rows, (lo, hi) in ((m, bytes_a), (n, bytes_b)):
+        codes = rng.integers(0, 16, (rows, k))
+        sb = rng.integers(lo, hi + 1, (rows, k // R.GROUP[scales]))
+        t = torch.from_numpy(R.tiles(sb)).cuda()
+        out.append((torch.from_numpy(R.pack(codes)).cuda(), t.view(torch.float8_e4m3fn) if scales == "e4m3" else t,
+                    torch.from_numpy(R.values(codes, sb, scales)).cuda()))
+    (a, a_s, av), (b, b_s, bv) = out
+    return sdq.matmul_fp4(a, a_s, b, b_s, out_dtype=torch.float32).double(), av @ bv.t(), av.abs() @ bv.abs().t()
+
+
+@pytest.mark.parametrize("m,n,k", [(7, 70, 320), (70, 300, 6240), (1700, 1600, 288)])
+@pytest.mark.parametrize("scales,bytes_a,bytes_b", [("e8m0", (0, 6), (248, 254)), ("e8m0", (248, 254), (0, 6)), ("e8m0", (0, 4), (127, 130)),
+                                                    ("e8m0", (180, 184), (170, 174)), ("e4m3", (0, 7), (0, 7)),
+                                                    ("e4m3", (0, 9), (120, 126)), ("e4m3", (120, 126), (120, 126))])
+def test_product_of_the_largest_and_smallest_scales(scales, bytes_a, bytes_b, m, n, k):
+    """Scales from the ends of their formats, alone and against the other end: sums that fp32 holds are right.  The
+    tolerance of test_fp4_gpu, and half of fp32's smallest step for each term where terms are subnormal."""
+    got, want, mag = _sums(m, n, k, scales, bytes_a, bytes_b, m + k)
+    assert float(mag.max()) < 3e38                         # (what the inputs are chosen for)
+    assert ((got - want).abs() <= (k / 16 + 2) * 2.0 ** -23 * mag + k * 2.0 ** -150).all()
