@@ -120,6 +120,39 @@ int launch_pair(const Product& c, int sms) {
   return launch(fn, static_cast<unsigned>(2 * pairs), sdq::mm4::kPairThreads, Z::kSmem, c.stream, args);
 }
 
+// CTAs that share the steps along k, in a cluster.  In quarters of a step (a step
+// takes 0.3 us): the steps that are left to each, up to twice as long where two CTAs
+// share a multiprocessor, and the exchange of the sums, a third of a quarter for each
+// column and 16 more, twice that where eight CTAs of more than 32 columns exchange or
+// where the next call's CTAs find few multiprocessors free to start on.  Only
+// clusters that all fit at once: of four CTAs the device takes 33 (with one CTA a
+// multiprocessor; 34 took 1.6 times as long), of eight with more than 32 columns
+// fewer than 16.  us, E8M0 scales, with 1, 2, 4, 8 CTAs, the one chosen in brackets:
+//       1 x  4096 x 7168   10.4   7.0  [5.0]  5.9    61 x 7168 x  4096  [7.6]  8.2  14.5  28.0
+//       1 x  2048 x 1024    3.4   3.4  [2.9]  3.0    64 x 4096 x  7168  11.2   9.1  [8.7] 21.4
+//       1 x 16384 x 7168   10.7 [10.4]               64 x 2048 x 14336  19.4  13.1  [9.2] 16.0
+//      32 x  1024 x 7168   10.6   7.7   5.6  [4.4]  128 x 4096 x  7168  12.2 [11.3] 12.1  33.8
+//      32 x 16384 x 1024   [3.7]  6.0               256 x 1024 x  4096  [8.5]  9.4   9.3  20.2
+// Over 510 calls (1 to 256 rows, n 128 to 16384, k 512 to 14336) the one chosen takes
+// 0.6 % more than the best of the four, 22 % at the worst (32 x 5632 x 14336).
+int split_of(int cols, int64_t tiles, int64_t steps, int sms) {
+  const bool wide = cols > sdq::mm4::kNarrow;
+  int split = 1;
+  int64_t best = 4 * steps;
+  for (int s = 2; s <= 8 && s <= steps; s *= 2) {
+    const int64_t ctas = tiles * s;
+    const bool many = ctas > sms / 2;
+    if (ctas * (s > 2 ? 10 : 9) > 9 * (wide ? sms : 2 * sms) || (wide && s == 8 && many)) break;
+    const int64_t step = ctas <= sms ? 4 : s == 2 ? 7 : 8;
+    const int64_t cost = (steps + s - 1) / s * step + (cols + 16) / 12 * (wide && (many || s == 8) ? 8 : 4);
+    if (cost < best) {
+      best = cost;
+      split = s;
+    }
+  }
+  return split;
+}
+
 // Few rows of a, or few tiles: clusters that share the steps along k.
 template <Scales S>
 int launch_strip(const Product& c, int sms) {
@@ -151,14 +184,7 @@ int launch_strip(const Product& c, int sms) {
   if (const int e = limit.set(fn, 210 * 1024)) return e;
   const int64_t tiles = p.tiles_b * ((c.m + p.cols - 1) / p.cols);
   const int64_t steps = (c.k + sdq::mm4::kStepCodes - 1) / sdq::mm4::kStepCodes;
-  // CTAs that share the steps along k: as many as the device holds, while the
-  // steps saved outweigh the exchange of the sums.  Up to 32 columns that takes
-  // 1.5 us and a step 0.3 (1 x 4096 x 7168: 11.2, 8.2, 7.0, 7.0 us with 1, 2, 4,
-  // 8 CTAs); with more columns it grows (61 x 7168 x 4096, 16 steps: 9.0 us with
-  // one CTA and with two, 15.9 with four).
-  const bool narrow = p.cols <= sdq::mm4::kNarrow;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= (narrow ? 2 : 1) * sms && steps >= (narrow ? 4 : 24) * split) split *= 2;
+  const int split = split_of(p.cols, tiles, steps, sms);
   p.stages = Z::stages(p.cols, split);
   p.share = Z::share(p.cols, split);
   for (int s = p.share; s > 1; s /= 2) ++p.share_log;
@@ -172,8 +198,9 @@ int launch_product(const Product& c) {
   if (const int e = sdq_internal::sm_count(&sms)) return e;
   const bool e8m0 = c.format & SDQ_FMT_E8M0, f32 = c.format & SDQ_FMT_OUT_F32;
   // Tiles of 128 x 128 that the device takes at once: 128 columns a CTA keep more
-  // multiprocessors busy than 256 x 256 outputs a pair (256 x 1024 x 1024: 5.1 us
-  // instead of 5.7; 1024 x 1024 x 4096: 9.4 instead of 9.8).
+  // multiprocessors busy than 256 x 256 outputs a pair (300 x 513 x 768: 4.5 us
+  // instead of 7.1; 1024 x 1024 x 4096, 64 tiles: 8.6 and 9.2; 1024 x 2304 x 4096,
+  // 144: 9.0 and 9.4).
   if (c.m <= 128 || (c.m + 127) / 128 * ((c.n + 127) / 128) <= sms)
     return e8m0 ? launch_strip<Scales::kE8M0>(c, sms) : launch_strip<Scales::kE4M3>(c, sms);
   if (f32) return e8m0 ? launch_pair<Scales::kE8M0, true>(c, sms) : launch_pair<Scales::kE4M3, true>(c, sms);

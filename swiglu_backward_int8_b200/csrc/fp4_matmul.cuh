@@ -262,14 +262,13 @@ struct Alpha {
 // Reading B bounds it, and below some 8 MB the launch and the latencies in a row
 // (wait for the kernel before, first load, exchange, store: 5 us).  B's rows are the accumulator's lanes, 128 a CTA, and A's its
 // columns, so an instruction is no wider than A needs.  The CTAs of a cluster take
-// the steps along k in turn, so that there are about as many CTAs as the device
-// holds; each sends its sums to the CTA that a column belongs to (column c to rank
+// the steps along k in turn, where that is worth the exchange (split_of); each sends its sums to the CTA that a column belongs to (column c to rank
 // c / share), which adds them up in the order of the ranks: the result does not
 // depend on timing.  (Sending takes one barrier of the cluster; reading the
 // others' sums took two, and a latency a number.)  Up to 32 columns two CTAs fit a
 // multiprocessor: a kernel's set-up is under way while the one before it still
-// runs.  1 x 4096 x 7168: 6.6 us (9.7 with one CTA for all of k), of 2.5 that its
-// bytes take; 61 x 7168 x 4096: 9.0 us.
+// runs.  1 x 4096 x 7168: 5.0 us (10.4 with one CTA for all of k), of 2.5 that its
+// bytes take; 61 x 7168 x 4096: 7.8 us.
 
 // Where a lane's next output goes: its column of `out`, a row further each time.
 struct Column {

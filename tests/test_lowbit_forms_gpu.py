@@ -30,14 +30,15 @@ from tests.test_norm_gpu import U24, _rows
 pytestmark = pytest.mark.gpu
 
 
-# (m, n, k): CTAs that share the steps, columns a CTA.  The first of either kind have several blocks of B or rows of
-# tiles; 48 to 128 columns leave ranks with 8 to 64 of them, some with none.
-SPLIT = [(48, 300, 7168), (64, 4096, 7168), (100, 257, 6176), (128, 130, 7168), (300, 513, 7168),   # 2, more than 32 columns
-         (70, 40, 12320),                                                                           # 4
-         (90, 130, 24608),                                                                          # 8
-         (17, 100, 1344), (32, 260, 1056),                                                          # 2, up to 32 columns
-         (9, 200, 3360), (20, 140, 2080),                                                           # 4
-         (9, 200, 4096), (30, 129, 8192), (16, 129, 4128)]                                          # 8
+# (m, n, k): by the CTAs that share the steps on 148 multiprocessors, and the columns a CTA.  Some have several blocks
+# of B or rows of tiles; ranks have 4 to 64 of the columns, some none.
+SPLIT = [(128, 4096, 7168), (100, 3000, 6176),                                                       # 2, more than 32 columns
+         (48, 300, 7168), (64, 4096, 7168), (100, 257, 6176), (128, 130, 7168), (300, 513, 7168), (70, 40, 12320),   # 4
+         (90, 130, 24608), (128, 900, 30016),                                                       # 8
+         (9, 7168, 4096), (20, 5632, 4096),                                                         # 2, up to 32 columns
+         (5, 100, 800), (1, 4096, 7168),                                                            # 4
+         (9, 200, 3360), (20, 140, 2080), (9, 200, 4096), (30, 129, 8192), (16, 129, 4128),         # 8
+         (17, 100, 1344), (32, 260, 1056), (61, 7168, 4096)]                                        # 1
 
 
 @pytest.mark.parametrize("scales", ["e8m0", "e4m3"])
