@@ -135,3 +135,24 @@ def test_norm_repeats_bit_for_bit(rows, channels):
     for _ in range(8):
         for a, b in zip(sdq.rmsnorm_quant(x, w, r, codes="e4m3"), first):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("rows,channels", [(3, 7168), (1, 48), (700, 1408), (4000, 96), (900, 16384), (2, 16400), (3, 1 << 17)])
+def test_norm_within_the_bound_of_its_order_of_sums(rows, channels):
+    """A thread adds the squares of 16 channels, eight in each lane of a pair, then the two lanes, then its vectors (one,
+    or every 1024th of a row past 16384 channels), then ten levels of shuffles: (18 + v) u of the sum.  1 / channels,
+    the mean and eps round once each, half of all that reaches rstd; the root's approximation with a Newton step adds
+    1.5 u (and the square of 2^-22), the two products of y one each, a group's scale one more."""
+    gen = torch.Generator(device="cuda").manual_seed(rows + channels)
+    x = _rows(gen, rows, channels, 1.3)
+    w = torch.randn(channels, generator=gen, device="cuda")
+    rstd = torch.empty(rows, device="cuda")
+    _, s, _ = sdq.rmsnorm_quant(x, w, group_size=32, rstd=rstd)
+    d = x.double()
+    want = 1 / (d.square().mean(1) + 1e-6).sqrt()
+    v = 1 if channels <= 16384 else -(-channels // 16384)
+    bound = (21 + v) / 2 + 1.6
+    assert ((rstd.double() / want - 1).abs() <= bound * U24).all(), float((rstd.double() / want - 1).abs().max() / U24)
+    y = torch.nn.functional.pad(d * want[:, None] * w.double(), (0, -channels % 32))
+    top = y.abs().reshape(rows, -1, 32).amax(2) / 127
+    assert ((s.double() / top - 1).abs() <= (bound + 3.1) * U24).all(), float((s.double() / top - 1).abs().max() / U24)
