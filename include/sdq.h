@@ -354,7 +354,8 @@ int sdq_validate_swiglu_q8_1(const void* gate, int64_t ld_gate, const void* up, 
  *   rows 0 <= rows <= SDQ_MAX_M (0: no-op); channels a multiple of
  *   SDQ_K_MULTIPLE (E2M1: SDQ_FP4_K_MULTIPLE), at most SDQ_MAX_K; leading
  *   dimensions at most SDQ_MAX_LD_NORM.
- * Sums are fp32: a row whose squares add up past 3.4e38 has rstd 0.
+ * Sums are fp32: a row whose squares add up past 3.4e38 has rstd 0, and one whose
+ * squares are below 2^-126 (it matters with an eps as small) loses bits.
  * One kernel on `stream`; allocates nothing.  Errors as sdq_fuse_strided.
  */
 int sdq_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,

@@ -10,11 +10,14 @@
 // memory.
 //
 // 2 bytes are read and 0.53 or 0.56 written a value and axis.  Along the rows DRAM
-// bounds it (8192 x 4096: 15 to 17 us, 77 to 85 % of the measured copy's rate);
-// along both axes instructions do (E8M0 scales 22.2 us, 72 %; E4M3 scales, twice
-// the groups and a Newton step a quotient, 26.3, 62 %): 16 a value, 59 % of the issue
-// slots by 24 warps, half of them in the half-rate integer pipe, which unpacks,
-// converts and compares.  Reading back: 15.3 us, 85 %.
+// bounds it (8192 x 4096: 14.5 to 15 us in short runs, 86 to 91 % of the measured
+// copy's rate); along the columns (E8M0 scales 18.2 us, E4M3 20.1) and both axes
+// instructions do (E8M0 scales 21.9 us, 72 %; E4M3 scales, twice the groups and a
+// Newton step a quotient, 26 to 27, 60 %): 16 a value, 59 % of the issue slots by 24
+// warps, half of them in the half-rate integer pipe, which unpacks, converts and
+// compares.  Groups of zeros go the way of unusual scales: a tensor of them takes up
+// to a fifth longer (both axes, E8M0 26.5 us, E4M3 29.9).  Reading back: 12.9 us in
+// short runs, 15 among other calls.
 #pragma once
 
 #include <cstdint>
@@ -60,6 +63,7 @@ __device__ __forceinline__ void store_scale_tiles(const uint8_t* sc, uint8_t* ou
 
 // CTAs a multiprocessor: four, but three where the columns' groups of 32, or both
 // axes, need more registers (both axes, E8M0 scales: 22 us with three, 29 with four).
+// Rows alone with E8M0 scales spill 48 bytes at four.
 template <Scales S, bool kRows, bool kCols>
 __global__ void __launch_bounds__(kThreads, kCols && (kRows || S == Scales::kE8M0) ? 3 : 4) quantize_kernel(const QuantParams p) {
   constexpr int G = S == Scales::kE8M0 ? 32 : 16;

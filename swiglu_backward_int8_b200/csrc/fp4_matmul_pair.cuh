@@ -15,9 +15,9 @@
 //
 // What bounds it: filling shared memory from L2.  A stage is 35 KB (38 with E4M3
 // scales) a multiprocessor, and 82 GB/s each (12 TB/s in all) is what the loads
-// reach with the products taken out: 170 of the 176 us of 8192 x 14336 x 4096 at
-// full clock (5.5 PFLOP/s).  Back to back for a second the power limit lowers the
-// clock: 205 us (4.7 PFLOP/s).
+// reach with the products taken out: 170 of the 175 us of 8192 x 14336 x 4096 at
+// full clock (5.5 PFLOP/s; with E4M3 scales 185).  Back to back for a second the
+// power limit lowers the clock: 208 us (4.6 PFLOP/s).
 #pragma once
 
 #include "fp4_matmul.cuh"

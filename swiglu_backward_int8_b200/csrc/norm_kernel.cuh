@@ -14,11 +14,13 @@
 //
 // One pass over the arrays, a row in a CTA's registers (several short rows to a
 // warp or a CTA); longer rows are read again from L2.  DRAM bounds long calls:
-// 16384 x 7168, residual, E4M3 codes, one scale for 128 channels, 132 us, 95 % of
-// the measured copy's rate; the backward of 16384 x 4096, 92 us, 89 %, of 16384 x
-// 7168, 176 us, 82 % (14 warps a multiprocessor, by registers).  Short calls are
-// bound by the row's latency (load, sum over the CTA, scale, store) and the
-// launch: 1 x 7168, 2.9 us; the backward of 517 x 7168, 9.2 us.
+// 16384 x 7168, residual, E4M3 codes, one scale for 128 channels, 127 us in short
+// runs, 99 % of the measured copy's rate, and 138 sustained; the backward of 16384 x
+// 4096, 87 and 96 us, 94 %, of 16384 x 7168, 168 us in short runs, 86 % (14 warps a
+// multiprocessor, by registers).  Rows that are read again: 4096 x 20480 171 us,
+// half the rate, the backward 230.  Short calls are bound by the row's latency
+// (load, sum over the CTA, scale, store) and the launch: 1 x 7168, 2.9 us; the
+// backward of 517 x 7168, 9.2 us.
 #pragma once
 
 #include <cstdint>
@@ -498,6 +500,8 @@ __device__ __forceinline__ void rmsnorm_backward(const BwdParams& p, int threads
 }
 
 // Registers a thread, and with them warps a quarter of a multiprocessor: 8, 6, 4.
+// (Two vectors in several rows a CTA spill 8 bytes, four vectors 48: a register
+// more a thread is two warps fewer.)
 constexpr int backward_regs(int vecs) { return vecs == 1 ? 64 : vecs == 2 ? 80 : 128; }
 
 template <int kVecs, bool kSeveral>
