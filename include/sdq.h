@@ -377,7 +377,9 @@ int sdq_validate_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual
  *   n = h * rstd,  g = grad_y * weight
  *   grad_x[m, k]   = bf16(rstd[m] * (g - n * mean_k(g * n)) + grad_h[m, k])
  *   grad_weight[k] = sum_m grad_y[m, k] * n[m, k]                       fp32
- * grad_x is the gradient of x and of residual alike.
+ * grad_x is the gradient of x and of residual alike.  (The mean is the row's fp32
+ * sum of grad_y * weight * h, then times rstd / channels: that sum has to lie
+ * inside fp32's range.)
  *   grad_y, h      bf16 [rows, channels]; h as sdq_rmsnorm_quant wrote it (x
  *                  without a residual); rstd fp32 [rows] likewise
  *   grad_h         bf16, the gradient that reaches h past the norm, or NULL
